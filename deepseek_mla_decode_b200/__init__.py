@@ -49,7 +49,19 @@ EXPORTED_SYMBOLS = (
     "mla_get_metadata_tokens",
     "mla_decode_tokens",
     "mla_decode_fp8_tokens",
+    "mla_rope_init",
+    "mla_rope_q",
+    "mla_rope_inplace",
+    "mla_append_kv",
+    "mla_append_kv_fp8",
 )
+
+
+class Rope(ctypes.Structure):
+    """mla_rope_t: a rotation's 32 frequencies (radians a position), amplitude and layout."""
+
+    _fields_ = [("freq", ctypes.c_double * 32), ("amplitude", ctypes.c_float), ("half_layout", ctypes.c_int32)]
+
 
 _lib = None
 
@@ -116,6 +128,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.mla_decode_noalloc.restype = c_int
     L.mla_decode_noalloc.argtypes = [c_vp, c_vp, c_vp, c_i64, c_vp, c_int, c_vp, c_int, c_int, c_int, c_f, c_int,
                                      c_vp, c_size, c_vp, c_vp, c_vp, c_vp]
+    p_rope = ctypes.POINTER(Rope)
+    c_d = ctypes.c_double
+    L.mla_rope_init.restype = c_int
+    L.mla_rope_init.argtypes = [p_rope, c_d, c_int, c_int, c_d, c_d, c_d, c_d, c_d]
+    L.mla_rope_q.restype = c_int
+    L.mla_rope_q.argtypes = [c_vp, c_i64, c_vp, c_vp, c_int, c_int, c_int, p_rope, c_vp, c_vp, c_vp, c_vp]
+    L.mla_rope_inplace.restype = c_int
+    L.mla_rope_inplace.argtypes = [c_vp, c_i64, c_vp, c_vp, c_int, c_int, c_int, p_rope, c_vp, c_vp]
+    for fn in (L.mla_append_kv, L.mla_append_kv_fp8):
+        fn.restype = c_int
+        fn.argtypes = [c_vp, c_i64, c_vp, c_f, c_vp, c_int, c_vp, c_vp, c_int, c_int, p_rope, c_vp, c_i64, c_vp, c_vp]
     L.mla_decode_combine.restype = c_int
     L.mla_decode_combine.argtypes = [c_vp, c_int, c_int, c_int, c_int, c_vp, c_size, c_vp, c_size, c_vp, c_vp,
                                      c_vp, c_vp]
@@ -419,6 +442,155 @@ def quantize_kv_fp8(kv_cache, kv_fp8=None, stream=None):
     _check("mla_quantize_kv_fp8", load_library().mla_quantize_kv_fp8(kv_cache.data_ptr(), kv_fp8.data_ptr(), rows,
                                                                      _stream_ptr(stream)))
     return kv_fp8
+
+
+_ROPE_SCALING = {"none": 0, "linear": 1, "yarn": 2}
+_ROPE_LAYOUT = {"interleaved": 0, "half": 1}
+
+
+def rope_params(base: float = 10000.0, layout: str = "interleaved", scaling: str = "none", factor: float = 1.0,
+                original_len: float = 4096.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                amplitude: float = 1.0) -> Rope:
+    """mla_rope_init: the rotation of a model's configuration.  layout "interleaved" pairs
+    (x[2i], x[2i+1]), "half" (x[i], x[i+32]); scaling "none", "linear" or "yarn"."""
+    if layout not in _ROPE_LAYOUT or scaling not in _ROPE_SCALING:
+        raise ValueError("layout 'interleaved' or 'half' and scaling 'none', 'linear' or 'yarn' expected")
+    r = Rope()
+    _check("mla_rope_init", load_library().mla_rope_init(
+        ctypes.byref(r), base, _ROPE_LAYOUT[layout], _ROPE_SCALING[scaling], factor, original_len, beta_fast,
+        beta_slow, amplitude))
+    return r
+
+
+def _on_device(ref, named, stream):
+    """Checks the (name, tensor, dtype, shape) of `named` (None tensors are skipped; shape
+    None: any) against the CUDA device of `ref`, and returns the stream to launch on: the
+    given one, or that device's current one.  The device must be the current one."""
+    import torch
+
+    dev = ref.device
+    if dev.type != "cuda":
+        raise ValueError("CUDA tensors expected")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t, dtype, shape in named:
+        if t is None:
+            continue
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream
+
+
+def _token_rows(name, t, width):
+    """[B, s_q, ...] rows of `width` elements, contiguous in themselves and evenly spaced
+    (as a column slice of a fused projection is); returns (B, s_q, elements a row)."""
+    B, s_q = t.shape[:2]
+    inner, want = t.stride()[2:], []
+    step = 1
+    for d in reversed(t.shape[2:]):
+        want.insert(0, step)
+        step *= d
+    if any(s != w and d != 1 for s, w, d in zip(inner, want, t.shape[2:])):
+        raise ValueError(f"{name}: the last dimensions must be contiguous")
+    row = t.stride(1) if s_q > 1 else (t.stride(0) if B > 1 else width)
+    if B > 1 and s_q > 1 and t.stride(0) != s_q * row:
+        raise ValueError(f"{name}: the tokens must be evenly spaced (one row stride over [B, s_q])")
+    return B, s_q, row
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def rope_q(q, cache_seqlens, rope: Rope, q_lens=None, q_heads=None, q_pe=None, status=None, stream=None):
+    """mla_rope_q: splits query heads q [B, s_q, H, 192] = [128 | 64 rotary] into q_heads
+    [B, s_q, H, 128] (for absorb_q) and q_pe [B, s_q, H, 64] (for decode), the latter rotated
+    at each token's position.  q may be a column slice of a wider projection."""
+    import torch
+
+    if q.dim() != 4 or q.shape[3] != 192 or q.dtype != torch.bfloat16:
+        raise ValueError("bf16 q [B, s_q, H, 192] expected")
+    H = q.shape[2]
+    B, s_q, row = _token_rows("q", q, H * 192)
+    if q_heads is None:
+        q_heads = torch.empty((B, s_q, H, 128), dtype=torch.bfloat16, device=q.device)
+    if q_pe is None:
+        q_pe = torch.empty((B, s_q, H, 64), dtype=torch.bfloat16, device=q.device)
+    s = _on_device(q, (("cache_seqlens", cache_seqlens, torch.int32, (B,)), ("q_lens", q_lens, torch.int32, (B,)),
+                       ("q_heads", q_heads, torch.bfloat16, (B, s_q, H, 128)),
+                       ("q_pe", q_pe, torch.bfloat16, (B, s_q, H, 64)), ("status", status, torch.int32, None)), stream)
+    _check("mla_rope_q", load_library().mla_rope_q(
+        q.data_ptr(), row, cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, ctypes.byref(rope), q_heads.data_ptr(),
+        q_pe.data_ptr(), _ptr(status), s))
+    return q_heads, q_pe
+
+
+def rope_inplace(q, cache_seqlens, rope: Rope, q_lens=None, status=None, stream=None):
+    """mla_rope_inplace: rotates the last 64 of each head of q [B, s_q, H, 192] where they
+    lie; returns q."""
+    import torch
+
+    if q.dim() != 4 or q.shape[3] != 192 or q.dtype != torch.bfloat16:
+        raise ValueError("bf16 q [B, s_q, H, 192] expected")
+    H = q.shape[2]
+    B, s_q, row = _token_rows("q", q, H * 192)
+    s = _on_device(q, (("cache_seqlens", cache_seqlens, torch.int32, (B,)), ("q_lens", q_lens, torch.int32, (B,)),
+                       ("status", status, torch.int32, None)), stream)
+    _check("mla_rope_inplace", load_library().mla_rope_inplace(
+        q.data_ptr(), row, cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, ctypes.byref(rope), _ptr(status), s))
+    return q
+
+
+def _append(fn, kv_a, cache, width, dtype, block_table, cache_seqlens, rope, norm_weight, eps, q_lens, status, stream):
+    import torch
+
+    if kv_a.dim() != 3 or kv_a.shape[2] != 576 or kv_a.dtype != torch.bfloat16:
+        raise ValueError("bf16 kv_a [B, s_q, 576] expected")
+    if cache.dim() != 3 or tuple(cache.shape[1:]) != (64, width):
+        raise ValueError(f"cache [num_blocks, 64, {width}] expected")
+    if block_table.dim() != 2:
+        raise ValueError("block_table [B, max_blocks] expected")
+    B, s_q, row = _token_rows("kv_a", kv_a, 576)
+    s = _on_device(kv_a, (("cache", cache, dtype, None),
+                          ("block_table", block_table, torch.int32, (B, block_table.shape[1])),
+                          ("cache_seqlens", cache_seqlens, torch.int32, (B,)), ("q_lens", q_lens, torch.int32, (B,)),
+                          ("norm_weight", norm_weight, torch.bfloat16, (512,)), ("status", status, torch.int32, None)),
+                   stream)
+    _check(fn, getattr(load_library(), fn)(
+        kv_a.data_ptr(), row, _ptr(norm_weight), eps, block_table.data_ptr(), block_table.shape[1],
+        cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, ctypes.byref(rope) if rope is not None else None,
+        cache.data_ptr(), cache.shape[0], _ptr(status), s))
+    return cache
+
+
+def append_kv(kv_a, kv_cache, block_table, cache_seqlens, rope: Optional[Rope] = None, norm_weight=None,
+              eps: float = 1e-6, q_lens=None, status=None, stream=None):
+    """mla_append_kv: writes the new tokens' rows kv_a [B, s_q, 576] = [c | k] into the paged
+    bf16 cache [num_blocks, 64, 576]: c normalised by norm_weight (if given), k rotated by
+    rope (if given).  cache_seqlens counts the new tokens.  Returns kv_cache."""
+    import torch
+
+    return _append("mla_append_kv", kv_a, kv_cache, 576, torch.bfloat16, block_table, cache_seqlens, rope, norm_weight,
+                   eps, q_lens, status, stream)
+
+
+def append_kv_fp8(kv_a, kv_fp8, block_table, cache_seqlens, rope: Optional[Rope] = None, norm_weight=None,
+                  eps: float = 1e-6, q_lens=None, status=None, stream=None):
+    """mla_append_kv_fp8: append_kv into the packed FP8 cache [num_blocks, 64, 656] (uint8)."""
+    import torch
+
+    return _append("mla_append_kv_fp8", kv_a, kv_fp8, 656, torch.uint8, block_table, cache_seqlens, rope, norm_weight,
+                   eps, q_lens, status, stream)
 
 
 def decode_attention(q_nope, q_pe, kv_cache, block_table, cache_seqlens, softmax_scale: float, causal: bool,

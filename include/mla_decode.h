@@ -377,6 +377,92 @@ mla_status_t mla_sage_prefill(const void* q, const void* k, const void* v, int S
                               void* workspace, size_t workspace_bytes, void* out, float* lse, int32_t* status,
                               void* stream);
 
+/*
+ * Rotary positions.  A rotation turns the 32 pairs of a 64-wide vector x at position p:
+ *     (a, b) -> amplitude * (a cos t - b sin t, a sin t + b cos t),   t = p * freq[i]
+ * with (a, b) = (x[2i], x[2i + 1]) or, with half_layout, (x[i], x[i + 32]); the result is in
+ * the same layout.  Angles are formed and reduced in 64 bits, the rotation is fp32, the
+ * result is rounded once.  A mla_rope_t is host memory, read before the call returns; fill
+ * it with mla_rope_init or by hand (|freq| <= 1e6 radians a position, finite amplitude).
+ *
+ * mla_rope_init: freq[i] = base^(-i/32), then
+ *   MLA_ROPE_PLAIN   as it is (factor and the rest are not looked at)
+ *   MLA_ROPE_LINEAR  divided by factor
+ *   MLA_ROPE_YARN    freq * (1 - g) + freq / factor * g with the ramp
+ *       g = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *       lo = max(0, floor d(beta_fast)), hi = min(63, ceil d(beta_slow)),
+ *       d(r) = 64 ln(original_len / (2 pi r)) / (2 ln base)
+ *     (YaRN, Peng et al. 2023: pairs that turn more than beta_fast times within the
+ *     original length keep their frequency, those below beta_slow are interpolated)
+ *   base > 1, factor > 0, original_len > 0, beta_fast >= beta_slow > 0, all finite.
+ *   amplitude is stored as given (1 for none; YaRN's attention temperature otherwise).
+ * Host only, no device call.
+ */
+typedef struct {
+  double freq[32];     /* radians a position of each pair */
+  float amplitude;     /* factor on the rotated values    */
+  int32_t half_layout; /* 0: pairs (2i, 2i + 1); 1: pairs (i, i + 32) */
+} mla_rope_t;
+
+#define MLA_ROPE_PLAIN 0
+#define MLA_ROPE_LINEAR 1
+#define MLA_ROPE_YARN 2
+
+mla_status_t mla_rope_init(mla_rope_t* rope, double base, int half_layout, int scaling, double factor,
+                           double original_len, double beta_fast, double beta_slow, double amplitude);
+
+/*
+ * New tokens.  The calls below work on up to s_q new tokens of each of B sequences, any
+ * s_q >= 1 (a decode step's one, a draft's few, a prompt's chunk).  cache_seqlens[b] = n_b
+ * counts them, q_lens[b] in [0, s_q] of them are real (NULL: s_q each), and token i has
+ * position n_b - q_lens[b] + i: the tokens, lengths and padding of mla_decode_ragged.  A
+ * token i >= q_lens[b] is padding; one whose position is negative (n_b < q_lens[b], an idle
+ * slot of a batch) has no place either.  n_b < 0 or q_lens[b] outside [0, s_q] sets
+ * MLA_DEVICE_ERR_SEQLEN.  B * s_q < 2^31.
+ *
+ * mla_rope_q: the rotary part of the query heads, split off and rotated.
+ *   q        bf16 [B * s_q][H][192], heads = [128 without position | 64 rotary]; consecutive
+ *            tokens are row_stride elements apart (>= H * 192, a multiple of 8)
+ *   q_heads  bf16 [B * s_q][H][128]  written: the input of mla_absorb_q
+ *   q_pe     bf16 [B * s_q][H][64]   written: the q_pe of mla_decode
+ *   Tokens without a place get zeros, those of a sequence with an invalid length or count
+ *   NaN.  1 <= H <= 65535; the outputs must not overlap q.
+ * mla_rope_inplace: rotates the 64 of each head of q where they lie (for the quantised
+ *   prefill's q and k); the 128 are not touched.
+ * All pointers are device pointers, 16-byte aligned; asynchronous on `stream`.
+ */
+mla_status_t mla_rope_q(const void* q, int64_t row_stride, const int32_t* cache_seqlens, const int32_t* q_lens, int B,
+                        int s_q, int H, const mla_rope_t* rope, void* q_heads, void* q_pe, int32_t* status,
+                        void* stream);
+mla_status_t mla_rope_inplace(void* q, int64_t row_stride, const int32_t* cache_seqlens, const int32_t* q_lens, int B,
+                              int s_q, int H, const mla_rope_t* rope, int32_t* status, void* stream);
+
+/*
+ * Appending the new tokens' rows to the paged cache (tokens and lengths as above).
+ *   kv_a         bf16 [B * s_q][576] = [c | k] as the down-projection leaves it, consecutive
+ *                tokens row_stride elements apart (>= 576, a multiple of 8)
+ *   norm_weight  bf16 [512], or NULL: c is stored as it is; else c * w / sqrt(mean(c^2) + eps)
+ *   rope         NULL: k is stored as it is; else rotated at the token's position p
+ *   row          p % 64 of block block_table[b][p / 64] is written; the table covers n_b
+ * mla_append_kv: the bf16 cache [num_blocks][64][576], rounded once.
+ * mla_append_kv_fp8: the packed FP8 cache [num_blocks][64][656], scale, codes and keys from
+ *   the fp32 row as mla_quantize_kv_fp8 takes them from a bf16 row (which is what they are,
+ *   byte for byte, without norm and rotation).  A row with a NaN gets a NaN scale.
+ * Nothing but the rows of real tokens with a place is written.  A sequence with an invalid
+ * length or count, or n_b > max_blocks * 64 (MLA_DEVICE_ERR_SEQLEN), is left as it was, and
+ * so is a token whose block id lies outside [0, num_blocks) (MLA_DEVICE_ERR_BLOCK_ID).  Two
+ * tokens must not share a cache row (which one it holds then is not defined).  Device
+ * pointers, 16-byte aligned; asynchronous on `stream`.
+ */
+mla_status_t mla_append_kv(const void* kv_a, int64_t row_stride, const void* norm_weight, float eps,
+                           const int32_t* block_table, int max_blocks, const int32_t* cache_seqlens,
+                           const int32_t* q_lens, int B, int s_q, const mla_rope_t* rope, void* kv_cache,
+                           int64_t num_blocks, int32_t* status, void* stream);
+mla_status_t mla_append_kv_fp8(const void* kv_a, int64_t row_stride, const void* norm_weight, float eps,
+                               const int32_t* block_table, int max_blocks, const int32_t* cache_seqlens,
+                               const int32_t* q_lens, int B, int s_q, const mla_rope_t* rope, void* kv_fp8,
+                               int64_t num_blocks, int32_t* status, void* stream);
+
 /* Number of streaming multiprocessors the schedule targets on the current device.
  * Library convenience: no passage of the source pages corresponds to it. */
 mla_status_t mla_device_sm_count(int* sm_count);
