@@ -54,6 +54,9 @@ EXPORTED_SYMBOLS = (
     "mla_rope_inplace",
     "mla_append_kv",
     "mla_append_kv_fp8",
+    "mla_get_metadata_window",
+    "mla_decode_window",
+    "mla_decode_fp8_window",
 )
 
 
@@ -128,6 +131,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.mla_decode_noalloc.restype = c_int
     L.mla_decode_noalloc.argtypes = [c_vp, c_vp, c_vp, c_i64, c_vp, c_int, c_vp, c_int, c_int, c_int, c_f, c_int,
                                      c_vp, c_size, c_vp, c_vp, c_vp, c_vp]
+    L.mla_get_metadata_window.restype = c_int
+    L.mla_get_metadata_window.argtypes = [c_vp, c_vp, c_int, c_int, c_int, c_int, c_int, c_vp, c_size, c_vp]
+    for fn in (L.mla_decode_window, L.mla_decode_fp8_window):
+        fn.restype = c_int
+        fn.argtypes = [c_vp, c_vp, c_vp, c_i64, c_vp, c_int, c_vp, c_vp, c_int, c_int, c_int, c_f, c_int, c_int,
+                       c_vp, c_size, c_vp, c_size, c_vp, c_vp, c_vp, c_vp]
     p_rope = ctypes.POINTER(Rope)
     c_d = ctypes.c_double
     L.mla_rope_init.restype = c_int
@@ -591,6 +600,71 @@ def append_kv_fp8(kv_a, kv_fp8, block_table, cache_seqlens, rope: Optional[Rope]
 
     return _append("mla_append_kv_fp8", kv_a, kv_fp8, 656, torch.uint8, block_table, cache_seqlens, rope, norm_weight,
                    eps, q_lens, status, stream)
+
+
+def get_metadata_window(cache_seqlens, q_lens, s_q: int, H: int, window: int, sinks: int, metadata=None, stream=None):
+    """mla_get_metadata_window: the schedule for decode_window / decode_fp8_window (shared by
+    every layer of a step); q_lens may be None."""
+    import torch
+
+    B = cache_seqlens.shape[0]
+    if metadata is None:
+        metadata = torch.empty(metadata_size(B * s_q, 1, H) // 4, dtype=torch.int32, device=cache_seqlens.device)
+    s = _on_device(cache_seqlens, (("cache_seqlens", cache_seqlens, torch.int32, (B,)),
+                                   ("q_lens", q_lens, torch.int32, (B,)), ("metadata", metadata, torch.int32, None)),
+                   stream)
+    _check("mla_get_metadata_window", load_library().mla_get_metadata_window(
+        cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, window, sinks, metadata.data_ptr(), 4 * metadata.numel(), s))
+    return metadata
+
+
+def _decode_window(fn, q_nope, q_pe, kv, width, dtype, block_table, cache_seqlens, q_lens, softmax_scale, window, sinks,
+                   metadata, workspace, out, lse, status, stream):
+    import torch
+
+    if q_nope.dim() != 4 or kv.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q_nope [B, s_q, H, 512], cache [num_blocks, 64, width], block_table [B, max_blocks] expected")
+    B, s_q, H, _ = q_nope.shape
+    bf16, i32 = torch.bfloat16, torch.int32
+    if workspace is None:
+        workspace = torch.empty(workspace_size(B * s_q, 1, H), dtype=torch.uint8, device=q_nope.device)
+    if out is None:
+        out = torch.empty((B, s_q, H, 512), dtype=bf16, device=q_nope.device)
+    if lse is None:
+        lse = torch.empty((B, s_q, H), dtype=torch.float32, device=q_nope.device)
+    s = _on_device(q_nope, (
+        ("q_nope", q_nope, bf16, (B, s_q, H, 512)), ("q_pe", q_pe, bf16, (B, s_q, H, 64)),
+        ("cache", kv, dtype, (kv.shape[0], 64, width)), ("block_table", block_table, i32, (B, block_table.shape[1])),
+        ("cache_seqlens", cache_seqlens, i32, (B,)), ("q_lens", q_lens, i32, (B,)), ("metadata", metadata, i32, None),
+        ("workspace", workspace, torch.uint8, None), ("out", out, bf16, (B, s_q, H, 512)),
+        ("lse", lse, torch.float32, (B, s_q, H)), ("status", status, i32, None)), stream)
+    _check(fn, getattr(load_library(), fn)(
+        q_nope.data_ptr(), q_pe.data_ptr(), kv.data_ptr(), kv.shape[0], block_table.data_ptr(), block_table.shape[1],
+        cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, softmax_scale, window, sinks, metadata.data_ptr(),
+        4 * metadata.numel(), workspace.data_ptr(), workspace.numel(), out.data_ptr(), lse.data_ptr(), _ptr(status), s))
+    return out, lse
+
+
+def decode_window(q_nope, q_pe, kv_cache, block_table, cache_seqlens, q_lens, softmax_scale: float, window: int,
+                  sinks: int, metadata, workspace=None, out=None, lse=None, status=None,
+                  stream=None) -> Tuple[object, object]:
+    """mla_decode_window: decode_tokens in which the token at position p sees the keys
+    t <= p with t > p - window or t < sinks (metadata from get_metadata_window with the same
+    q_lens, window and sinks).  Returns (out bf16 [B, s_q, H, 512], lse fp32 [B, s_q, H])."""
+    import torch
+
+    return _decode_window("mla_decode_window", q_nope, q_pe, kv_cache, 576, torch.bfloat16, block_table, cache_seqlens,
+                          q_lens, softmax_scale, window, sinks, metadata, workspace, out, lse, status, stream)
+
+
+def decode_fp8_window(q_nope, q_pe, kv_fp8, block_table, cache_seqlens, q_lens, softmax_scale: float, window: int,
+                      sinks: int, metadata, workspace=None, out=None, lse=None, status=None,
+                      stream=None) -> Tuple[object, object]:
+    """mla_decode_fp8_window: decode_window over a packed FP8 cache [num_blocks, 64, 656]."""
+    import torch
+
+    return _decode_window("mla_decode_fp8_window", q_nope, q_pe, kv_fp8, 656, torch.uint8, block_table, cache_seqlens,
+                          q_lens, softmax_scale, window, sinks, metadata, workspace, out, lse, status, stream)
 
 
 def decode_attention(q_nope, q_pe, kv_cache, block_table, cache_seqlens, softmax_scale: float, causal: bool,

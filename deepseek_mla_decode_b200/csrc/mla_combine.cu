@@ -44,7 +44,7 @@ template <int kColParts, int kGroup, bool kBySeq>
 __global__ void __launch_bounds__(kWarps * 32) combine_kernel(
     const int32_t* __restrict__ meta, const int32_t* __restrict__ seqlens, const int32_t* __restrict__ q_lens,
     int max_blocks, int B, int s_q, int M, const float* __restrict__ part_o, const float* __restrict__ part_lse,
-    __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int tok_rep, int tok_causal) {
+    __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int tok_rep, int tok_causal, int window, int sinks) {
   // launched as a programmatic dependent of the attention kernel: wait for it
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // Dependent round trips to memory: the partition's start (by partition only), then
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kWarps * 32) combine_kernel(
   }
   // rows written as NaN already: invalid length, or a schedule built for another length
   if (n < 0 || (int64_t)n > (int64_t)max_blocks * kBlockSize) return;
-  if (nblk != (n + kBlockSize - 1) / kBlockSize) return;
+  if (nblk != (window > 0 ? window_blocks(n, window, sinks).count : (n + kBlockSize - 1) / kBlockSize)) return;
   if (ql < 0 || ql > s_q) return;  // invalid query count: NaN rows written already
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wid = blockIdx.y * kWarps + warp;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kWarps * 32) combine_kernel(
 
 cudaError_t launch_combine(const int32_t* meta, const int32_t* seqlens, const int32_t* q_lens, int max_blocks,
                            int B, int s_q, int M, int P, const float* part_o, const float* part_lse, void* out, float* lse,
-                           cudaStream_t stream, int tok_rep, int tok_causal) {
+                           cudaStream_t stream, int tok_rep, int tok_causal, int window, int sinks) {
   // few sequences: long ones with many splits and few rows to merge
   const bool wide = B < kWideBatch;
   const bool by_seq = wide || B <= P;
@@ -182,12 +182,12 @@ cudaError_t launch_combine(const int32_t* meta, const int32_t* seqlens, const in
   __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out);
   if (wide)
     return cudaLaunchKernelEx(&cfg, combine_kernel<4, 16, true>, meta, seqlens, q_lens, max_blocks, B, s_q, M, part_o,
-                              part_lse, o, lse, tok_rep, tok_causal);
+                              part_lse, o, lse, tok_rep, tok_causal, window, sinks);
   if (by_seq)
     return cudaLaunchKernelEx(&cfg, combine_kernel<1, 2, true>, meta, seqlens, q_lens, max_blocks, B, s_q, M, part_o,
-                              part_lse, o, lse, tok_rep, tok_causal);
+                              part_lse, o, lse, tok_rep, tok_causal, window, sinks);
   return cudaLaunchKernelEx(&cfg, combine_kernel<1, 2, false>, meta, seqlens, q_lens, max_blocks, B, s_q, M, part_o,
-                            part_lse, o, lse, tok_rep, tok_causal);
+                            part_lse, o, lse, tok_rep, tok_causal, window, sinks);
 }
 
 }  // namespace mla

@@ -28,6 +28,14 @@
 // and the weights that enter PV (P' = bf16(e * scale)), and the row sums stay in the
 // unscaled weights e.
 //
+// Sliding window (kWin, always over the token schedule, so all rows of a unit are one
+// token's and see the same keys): the pieces run over the unit's visible blocks only
+// (window_blocks), whose hidden rows are a block's first or its last.  Hidden rows never
+// reach an accumulator, whatever they hold: their scores are masked, and their V rows are
+// not loaded -- the box starts at the first visible row or ends at the last one, the rest
+// of it lies outside the block and is zero-filled by the TMA, and the block's P row is
+// shifted to match.
+//
 // Warp roles, bf16 cache (384 threads): warps 0, 2, 3 = TMA producers (ring stage k is
 // issued by producer k % 3; warp 0 also loads Q), warp 1 = MMA issuer (leader CTA only)
 // and TMEM owner, warps 4..11 = softmax / correction / epilogue (thread = one row x 64
@@ -121,6 +129,7 @@ struct Params {
   // length, table row and query count (tok_q_lens, or tok_rep each) it takes.
   const int32_t* tok_q_lens;
   int tok_rep, tok_causal;
+  int window, sinks;  // kWin: keys in the window, first keys that stay visible; else 0
   const int32_t* meta;
   __nv_bfloat16* out;
   float* lse;
@@ -165,6 +174,7 @@ constexpr int kIdRing = 128;
 
 struct Piece {
   int b, k_lo, k_hi, split, n, qlen;
+  WindowBlocks w;  // kWin: what the block numbers [k_lo, k_hi) stand for
 };
 
 // Keys of sequence u: its length, or with a token schedule the length of token
@@ -182,9 +192,12 @@ __device__ __forceinline__ int64_t table_row(const Params& p, int u) {
   return p.tok_rep ? u / p.tok_rep : u;
 }
 
-// Block count of a sequence of n keys, or -1 when n is not a valid length for the table.
+// Block count of a sequence of n keys (kWin: of its visible ones), or -1 when n is not a
+// valid length for the table.
+template <bool kWin>
 __device__ __forceinline__ int expected_blocks(const Params& p, int n) {
   if (n < 0 || (int64_t)n > (int64_t)p.max_blocks * kBlockSize) return -1;
+  if constexpr (kWin) return window_blocks(n, p.window, p.sinks).count;
   return (n + kBlockSize - 1) / kBlockSize;
 }
 
@@ -203,6 +216,7 @@ __device__ __forceinline__ int query_len(const Params& p, int b) {
 // no block-table entry past ceil(n / 64) is ever read.  With per-sequence query counts,
 // a row tile that holds only padding tokens of a sequence (rows >= q_lens[b] * H) skips
 // that sequence too; producer warp 0 writes those rows (0 / -inf).
+template <bool kWin>
 struct PieceWalker {
   const Params* p;
   int cb, ck, be, ke;
@@ -228,7 +242,7 @@ struct PieceWalker {
       ck = 0;
       if (lo >= hi) continue;
       const int n = seq_len(*p, b);
-      if (expected_blocks(*p, n) != nb) continue;
+      if (expected_blocks<kWin>(*p, n) != nb) continue;
       const int ql = query_len(*p, b);
       if (ql < 0 || row0 >= ql * p->H) continue;
       pc.b = b;
@@ -237,6 +251,7 @@ struct PieceWalker {
       pc.split = part - first_part[b];
       pc.n = n;
       pc.qlen = ql;
+      if constexpr (kWin) pc.w = window_blocks(n, p->window, p->sinks);
       return true;
     }
     return false;
@@ -250,11 +265,23 @@ __device__ __forceinline__ int blocks_in_tile(const Piece& pc, int t) {
   const int r = pc.k_hi - pc.k_lo - t * kBlocksPerTile;
   return r < kBlocksPerTile ? r : kBlocksPerTile;
 }
-// valid keys (< n) in block kb of tile t
-__device__ __forceinline__ int rows_in_block(const Piece& pc, int t, int kb) {
-  const int key0 = (pc.k_lo + t * kBlocksPerTile + kb) * kBlockSize;
-  const int r = pc.n - key0;
-  return r < kBlockSize ? r : kBlockSize;
+// the block of the sequence's table behind a piece's block number
+template <bool kWin>
+__device__ __forceinline__ int table_block(const Piece& pc, int v) {
+  if constexpr (kWin) return window_block(pc.w, v);
+  return v;
+}
+// visible rows [lo, hi) of block kb of tile t (without a window: the keys < n)
+template <bool kWin>
+__device__ __forceinline__ void rows_in_block(const Piece& pc, int t, int kb, int* lo, int* hi) {
+  const int v = pc.k_lo + t * kBlocksPerTile + kb;
+  if constexpr (kWin) {
+    window_rows(pc.w, pc.n, v, lo, hi);
+  } else {
+    const int r = pc.n - v * kBlockSize;
+    *lo = 0;
+    *hi = r < kBlockSize ? r : kBlockSize;
+  }
 }
 
 __device__ __forceinline__ void set_status(const Params& p, int bits) {
@@ -432,11 +459,12 @@ __device__ __forceinline__ int clamp_block_id(const Params& p, int32_t id) {
 // current length (NaN and MLA_DEVICE_ERR_METADATA).  Partition `part` takes the
 // sequences b with b % P == part; the 32 lanes of one warp write this CTA's 64 rows
 // [y0, y0 + 64) of the row tile that starts at row0.
+template <bool kWin>
 __device__ __forceinline__ void write_orphan_rows(const Params& p, int part, int P, int row0, int y0, int lane) {
   const int32_t* nblk = p.meta + off_nblk();
   for (int b = part; b < p.B; b += P) {
     const int n = seq_len(p, b);
-    const int want = expected_blocks(p, n);
+    const int want = expected_blocks<kWin>(p, n);
     const int ql = query_len(p, b);
     const bool bad_len = want < 0 || ql < 0;
     const bool stale = !bad_len && nblk[b] != want;
@@ -459,7 +487,7 @@ __device__ __forceinline__ void write_orphan_rows(const Params& p, int part, int
 // ===========================================================================
 // the kernel
 // ===========================================================================
-template <bool kFp8>
+template <bool kFp8, bool kWin>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads, 1)
     mla_decode_kernel(const __grid_constant__ Params p) {
   using C = Cfg<kFp8>;
@@ -538,7 +566,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
   int T = p.meta[kHdrNumTiles];
   if (p.meta[kHdrMagic] != kMetaMagic || p.meta[kHdrB] != p.B || p.meta[kHdrSq] != p.s_q ||
       p.meta[kHdrH] != p.H || P * T * 2 != (int)gridDim.x || p.meta[kHdrTokens] != p.tok_rep ||
-      (p.tok_rep != 0 && p.meta[kHdrTokCausal] != p.tok_causal)) {
+      (p.tok_rep != 0 && p.meta[kHdrTokCausal] != p.tok_causal) || p.meta[kHdrWindow] != p.window ||
+      p.meta[kHdrSinks] != p.sinks) {
     if (tid == 0 && blockIdx.x == 0) set_status(p, kErrMetadata);
     T = 0;  // every role skips; the CTA still joins the cluster barriers below
   }
@@ -557,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       if constexpr (kFp8) regs_dec<kRegsIssue>();
       const int pi = (warp == 0) ? 0 : warp - 1;
       int32_t* idwin = ctrl.block_ids[pi];
-      PieceWalker walk(p, part, tile_row0);
+      PieceWalker<kWin> walk(p, part, tile_row0);
       uint32_t it = 0;
       bool ok = true;
       auto mine = [&]() { return (int)(it % kNumProducers) == pi; };
@@ -582,7 +611,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       int cur_base = 0, id_pending = 0, id_chunks = 0;
       const int32_t* bt = nullptr;
       auto fetch_id = [&](int i) -> int {
-        return (i < cur.k_hi - cur.k_lo) ? clamp_block_id(p, bt[cur.k_lo + i]) : 0;
+        return (i < cur.k_hi - cur.k_lo) ? clamp_block_id(p, bt[table_block<kWin>(cur, cur.k_lo + i)]) : 0;
       };
       auto ensure_ids = [&](int last) {  // make relative blocks <= last of `cur` readable
         while (last >= 32 * id_chunks) {
@@ -673,7 +702,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       // last block, with rv < 64 valid keys, is loaded from row rv - 64: the box's
       // first 64 - rv rows fall before the block and are zero-filled by the TMA, the
       // keys land in rows [64 - rv, 64).  No row past the sequence end is read, so
-      // the stage needs no zeroing; P of that block is stored shifted to match.
+      // the stage needs no zeroing; P of that block is stored shifted to match.  A block
+      // whose first rows lie before a window is loaded from its first visible row: the
+      // box's end falls behind the block and is zero-filled.
       auto issue_pv = [&](const Piece& pc, int base, int t) {
         const int nb = blocks_in_tile(pc, t);
         for (int h = 0; h < 2 && ok; ++h) {
@@ -683,7 +714,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
               continue;
             }
             const int id = idwin[(base + t * kBlocksPerTile + kb) % kIdRing];
-            const int rv = rows_in_block(pc, t, kb);
+            int lo, hi;
+            rows_in_block<kWin>(pc, t, kb, &lo, &hi);
+            const int row0 = hi < kBlockSize ? hi - kBlockSize : lo;
             uint32_t slot;
             ok = __shfl_sync(0xffffffffu, acquire(slot), 0);
             if (!ok) break;
@@ -691,12 +724,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
             if constexpr (kFp8) {  // one block's 128-column slab of codes (8 KB)
               const uint32_t fb = smem_u32(&ctrl.stg_full[slot]);
               expect_tx_if(lane == 0, fb, kStgBytes);
-              tma_load_3d_if(lane == 0, sStg + slot * kStgBytes, &p.tm_kv2, fb, d0, rv - kBlockSize, id);
+              tma_load_3d_if(lane == 0, sStg + slot * kStgBytes, &p.tm_kv2, fb, d0, row0, id);
             } else {
               const uint32_t fb = smem_u32(&ctrl.full[slot]);
               expect_tx_if(lane == 0 && leader, fb, 2 * kStageBytes);
               tma_load_4d_cg2_if(lane == 0, sRing + slot * kStageBytes, &p.tm_kv2, mapa_shared(fb, 0), 0,
-                                 rv - kBlockSize, d0 / 64, id);
+                                 row0, d0 / 64, id);
             }
             ++it;
           }
@@ -736,7 +769,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         for (int t = 0; t < nt && ok; ++t) {
           if (t == nt - 1 && have_nxt) {
             const int32_t* btn = p.block_table + table_row(p, nxt.b) * p.max_blocks;
-            id_next = (lane < nxt.k_hi - nxt.k_lo) ? clamp_block_id(p, btn[nxt.k_lo + lane]) : 0;
+            id_next = (lane < nxt.k_hi - nxt.k_lo) ? clamp_block_id(p, btn[table_block<kWin>(nxt, nxt.k_lo + lane)]) : 0;
           }
           if (t == 0 && pi == 0) load_q(cur, npieces);
           if (ok) {
@@ -763,7 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       if (ok && prv_t >= 0) issue_pv(prv, prv_base, prv_t);
       // With its loads issued, producer warp 0 writes the rows that no partition
       // covers while the last tiles are still being computed.
-      if (pi == 0) write_orphan_rows(p, part, P, tile_row0, tile_row0 + kRowsPerCta * (int)rank, lane);
+      if (pi == 0) write_orphan_rows<kWin>(p, part, P, tile_row0, tile_row0 + kRowsPerCta * (int)rank, lane);
     }
     // =======================================================================
     // MMA issuer (leader CTA only)
@@ -773,7 +806,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       // Every lane waits and the elected lane's predicate issues.  No full-warp
       // collective sits inside the loop, so lanes that leave it at different points
       // after a wait ran out cannot deadlock the warp; they meet again at teardown.
-      PieceWalker walk(p, part, tile_row0);
+      PieceWalker<kWin> walk(p, part, tile_row0);
       uint32_t slot = 0, phase = 0, qk_count = 0, pv_count = 0;
       int npieces = 0;
       bool ok = true;
@@ -823,14 +856,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
           for (int kb = 0; kb < nb && ok; ++kb) {
             ok = wait_bar(&ctrl, p, smem_u32(&ctrl.full[slot]), phase);
             if (!ok) break;
-            // the sequence's last block sits in rows [64 - rv, 64): skip whole zero steps
-            const int rv = rows_in_block(pc, t, kb);
-            const int ks0 = (kBlockSize - rv) >> 4;
+            // the sequence's last block sits in rows [64 - rv, 64), a window's first one in
+            // rows [0, 64 - lo): skip whole zero steps
+            int lo, hi;
+            rows_in_block<kWin>(pc, t, kb, &lo, &hi);
+            const int ks0 = (kBlockSize - hi) >> 4;
+            const int ks1 = kWin ? (kBlockSize - lo + 15) >> 4 : 4;
             const bool first = (t == 0 && kb == 0);
             const uint64_t a0 = dp0 + kb * kChunkD, b0 = dv0 + slot * kStageD;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_2sm_if(elected && ks >= ks0, tmem + kTmemO + 128 * h, a0 + 2 * ks, b0 + 128 * ks, kIdescPV,
+              umma_2sm_if(elected && ks >= ks0 && ks < ks1, tmem + kTmemO + 128 * h, a0 + 2 * ks, b0 + 128 * ks, kIdescPV,
                           !(first && ks == ks0));
             commit_2sm_if(elected, smem_u32(&ctrl.empty[slot]));
             next_stage();
@@ -875,7 +911,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       const int y0 = tile_row0 + kRowsPerCta * (int)rank;
       const uint32_t p_full_l = mapa_shared(smem_u32(&ctrl.p_full), 0);
       const uint32_t o_free_l = mapa_shared(smem_u32(&ctrl.o_free), 0);
-      PieceWalker walk(p, part, tile_row0);
+      PieceWalker<kWin> walk(p, part, tile_row0);
       Piece pc;
       uint32_t qk_count = 0, pv_count = 0;
       // ok: this thread's waits all completed.  go: the same for all 256 threads,
@@ -994,7 +1030,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         {
           const int32_t* bt = p.block_table + table_row(p, pc.b) * p.max_blocks;
           for (int k = pc.k_lo + st; k < pc.k_hi; k += kNumSoftmaxThreads) {
-            const int32_t id = bt[k];
+            const int32_t id = bt[table_block<kWin>(pc, k)];
             bad_ids |= (id < 0 || (int64_t)id >= p.num_blocks);
           }
         }
@@ -1022,6 +1058,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
           const int key0 = (pc.k_lo + t * kBlocksPerTile) * kBlockSize + 128 * hk + 64 * g;
           int cnt = lim - key0 + 1;
           cnt = cnt < 0 ? 0 : (cnt > 64 ? 64 : cnt);
+          // kWin: of this thread's block, keys [c0, c0 + cnt) are visible
+          int c0 = 0, hi = kBlockSize;
+          if constexpr (kWin) {
+            cnt = 0;
+            if (pc.k_lo + t * kBlocksPerTile + 2 * hk + g < pc.k_hi) {
+              rows_in_block<true>(pc, t, 2 * hk + g, &c0, &hi);
+              if (row_valid) cnt = hi - c0;
+            }
+          }
+          auto seen = [&](int c) -> bool {
+            if constexpr (kWin) return (uint32_t)(c - c0) < (uint32_t)cnt;
+            return c < cnt;
+          };
           // Tiles with every key visible (all but a sequence's last tile and causal
           // edges) take an unmasked path; the choice is warp-uniform.
           const bool full = __all_sync(0xffffffffu, cnt == kBlockSize);
@@ -1048,10 +1097,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
           } else {
 #pragma unroll
             for (int c = 0; c < 64; c += 4) {
-              if (c < cnt) mx0 = fmaxf(mx0, __uint_as_float(sr[c]));
-              if (c + 1 < cnt) mx1 = fmaxf(mx1, __uint_as_float(sr[c + 1]));
-              if (c + 2 < cnt) mx2 = fmaxf(mx2, __uint_as_float(sr[c + 2]));
-              if (c + 3 < cnt) mx3 = fmaxf(mx3, __uint_as_float(sr[c + 3]));
+              if (seen(c)) mx0 = fmaxf(mx0, __uint_as_float(sr[c]));
+              if (seen(c + 1)) mx1 = fmaxf(mx1, __uint_as_float(sr[c + 1]));
+              if (seen(c + 2)) mx2 = fmaxf(mx2, __uint_as_float(sr[c + 2]));
+              if (seen(c + 3)) mx3 = fmaxf(mx3, __uint_as_float(sr[c + 3]));
             }
           }
           const float lmax = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * (kFp8 ? 1.0f : sl2);
@@ -1081,7 +1130,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
             // lse); the PV operand is P' = bf16(e * scale_key), since V = scale_key * codes
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
-              const bool v0 = full || c < cnt, v1 = full || c + 1 < cnt;
+              const bool v0 = full || seen(c), v1 = full || seen(c + 1);
               const float e0 = v0 ? fast_exp2(__uint_as_float(sr[c]) + nref) : 0.f;
               const float e1 = v1 ? fast_exp2(__uint_as_float(sr[c + 1]) + nref) : 0.f;
               const float p0 = v0 ? e0 * scb[4 * c] : 0.f;
@@ -1113,10 +1162,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
             } else {
 #pragma unroll
               for (int c = 0; c < 64; c += 4) {
-                const float e0 = (c < cnt) ? fast_exp2(fmaf(__uint_as_float(sr[c]), sl2, nref)) : 0.f;
-                const float e1 = (c + 1 < cnt) ? fast_exp2(fmaf(__uint_as_float(sr[c + 1]), sl2, nref)) : 0.f;
-                const float e2 = (c + 2 < cnt) ? fast_exp2(fmaf(__uint_as_float(sr[c + 2]), sl2, nref)) : 0.f;
-                const float e3 = (c + 3 < cnt) ? fast_exp2(fmaf(__uint_as_float(sr[c + 3]), sl2, nref)) : 0.f;
+                const float e0 = seen(c) ? fast_exp2(fmaf(__uint_as_float(sr[c]), sl2, nref)) : 0.f;
+                const float e1 = seen(c + 1) ? fast_exp2(fmaf(__uint_as_float(sr[c + 1]), sl2, nref)) : 0.f;
+                const float e2 = seen(c + 2) ? fast_exp2(fmaf(__uint_as_float(sr[c + 2]), sl2, nref)) : 0.f;
+                const float e3 = seen(c + 3) ? fast_exp2(fmaf(__uint_as_float(sr[c + 3]), sl2, nref)) : 0.f;
                 const uint32_t v0 = pack_bf16x2(e0, e1), v1 = pack_bf16x2(e2, e3);
                 pk[c >> 1] = v0;
                 pk[(c >> 1) + 1] = v1;
@@ -1167,7 +1216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
           // of its V stage: shift its P row right by 64 - rv keys to match (the keys
           // shifted out are >= rv, whose weights are 0; zeros are shifted in).
           {
-            const int rv = pc.n - key0;
+            const int rv = kWin ? hi : pc.n - key0;
             if (rv > 0 && rv < kBlockSize) {  // warp-uniform: the warp's rows share the block
               const int sh = kBlockSize - rv;
               if (sh & 1) {
@@ -1181,6 +1230,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
                 if ((ws >> bit) & 1) {
 #pragma unroll
                   for (int w = 31; w >= 0; --w) pk[w] = (w >= (1 << bit)) ? pk[w - (1 << bit)] : 0u;
+                }
+              }
+            }
+          }
+          // A window's first block was loaded from its first visible row c0 on: shift its P
+          // row left by c0 keys (the keys shifted out are hidden, whose weights are 0).
+          if constexpr (kWin) {
+            if (c0 > 0) {  // warp-uniform
+              if (c0 & 1) {
+#pragma unroll
+                for (int w = 0; w < 31; ++w) pk[w] = __byte_perm(pk[w], pk[w + 1], 0x5432);
+                pk[31] >>= 16;
+              }
+              const int ws = c0 >> 1;
+#pragma unroll
+              for (int bit = 0; bit < 5; ++bit) {
+                if ((ws >> bit) & 1) {
+#pragma unroll
+                  for (int w = 0; w < 32; ++w) pk[w] = (w + (1 << bit) < 32) ? pk[w + (1 << bit)] : 0u;
                 }
               }
             }
@@ -1226,6 +1294,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         // a bad piece's rows become NaN: scaling by NaN turns every value into NaN
         pend_sc = bad ? nanf_ : ((l_row > 0.f) ? 1.f / l_row : 0.f);
         pend_lse = bad ? nanf_ : ((l32_row > 0.f) ? (m_used + __log2f(l32_row)) * 0.69314718055994531f : -INFINITY);
+        // kWin: a NaN among the visible scores shows in the lse too (and so survives the
+        // merge of a split sequence, which drops a piece whose lse is -inf)
+        if constexpr (kWin) pend_lse = (l32_row != l32_row) ? nanf_ : pend_lse;
         pend_direct = (nsplit == 1);
         pend_b = pc.b;
         pend_slot = split_base + pc.split;
@@ -1255,7 +1326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         const int grp = (tid - kConvWarp0 * 32) >> 6;  // 0, 1
         const int ct = (tid - kConvWarp0 * 32) & 63;   // 0..63 within the group
         constexpr int kGrpThreads = 64;
-        PieceWalker walk(p, part, tile_row0);
+        PieceWalker<kWin> walk(p, part, tile_row0);
         uint32_t js = 0, ir = 0;  // raw stages and ring slots consumed so far
         bool ok = true, go = true;
         auto wait_raw = [&](uint32_t j) {
@@ -1441,11 +1512,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
 
 cudaError_t decode_kernel_setup(int device) {
   (void)device;
-  cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg<false>::kSmemDyn + 1024);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(mla_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Cfg<true>::kSmemDyn + 1024);
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<false, false>, attr, Cfg<false>::kSmemDyn + 1024);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(mla_decode_kernel<true, false>, attr, Cfg<true>::kSmemDyn + 1024);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(mla_decode_kernel<false, true>, attr, Cfg<false>::kSmemDyn + 1024);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(mla_decode_kernel<true, true>, attr, Cfg<true>::kSmemDyn + 1024);
+  return e;
 }
 
 // tm_kpe / tm_scl: FP8 cache only (null for the bf16 cache, which fp8 = false selects).
@@ -1457,7 +1529,8 @@ cudaError_t launch_decode(bool fp8, const CUtensorMap& tm_kv, const CUtensorMap&
                           const int32_t* q_lens, const int32_t* meta, int64_t num_blocks, int B, int s_q,
                           int H, float scale, int causal, void* out, float* lse, float* part_o, float* part_lse,
                           int32_t* status, int num_ctas, uint64_t wait_timeout_ns, int inject_stall,
-                          cudaStream_t stream, int tok_rep, int tok_causal, const int32_t* tok_q_lens) {
+                          cudaStream_t stream, int tok_rep, int tok_causal, const int32_t* tok_q_lens, int window,
+                          int sinks) {
   if (fp8 && (!tm_kpe || !tm_scl)) return cudaErrorInvalidValue;
   Params prm;
   std::memset(&prm, 0, sizeof(prm));
@@ -1477,6 +1550,8 @@ cudaError_t launch_decode(bool fp8, const CUtensorMap& tm_kv, const CUtensorMap&
   prm.tok_q_lens = tok_q_lens;
   prm.tok_rep = tok_rep;
   prm.tok_causal = tok_causal;
+  prm.window = window;
+  prm.sinks = sinks;
   prm.meta = meta;
   prm.out = reinterpret_cast<__nv_bfloat16*>(out);
   prm.lse = lse;
@@ -1506,8 +1581,9 @@ cudaError_t launch_decode(bool fp8, const CUtensorMap& tm_kv, const CUtensorMap&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return fp8 ? cudaLaunchKernelEx(&cfg, mla_decode_kernel<true>, prm)
-             : cudaLaunchKernelEx(&cfg, mla_decode_kernel<false>, prm);
+  if (window > 0)
+    return cudaLaunchKernelEx(&cfg, fp8 ? mla_decode_kernel<true, true> : mla_decode_kernel<false, true>, prm);
+  return cudaLaunchKernelEx(&cfg, fp8 ? mla_decode_kernel<true, false> : mla_decode_kernel<false, false>, prm);
 }
 
 }  // namespace mla

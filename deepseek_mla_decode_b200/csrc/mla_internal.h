@@ -45,6 +45,8 @@ enum HdrField : int {
   kHdrOverhead = 9,
   kHdrTokens = 10,    // token schedule: the call's s_q (query tokens per sequence); 0 otherwise
   kHdrTokCausal = 11, // token schedule: the causal flag the lengths were built with
+  kHdrWindow = 12,    // windowed schedule: keys in the window; 0 otherwise
+  kHdrSinks = 13,     // windowed schedule: first keys that stay visible
 };
 constexpr int32_t kMetaMagic = 0x4D4C4131;  // "MLA1"
 
@@ -60,6 +62,43 @@ __host__ __device__ inline int token_seq_len(int n, int q, int t, int rep, int c
   if (!causal) return n;
   const int v = n - q + t + 1;
   return v > 0 ? v : 0;
+}
+
+// Sliding window.  The token at position n - 1 sees the keys t < n with t >= n - window or
+// t < sinks.  Its blocks are numbered through without the hidden ones: `sink_blocks` blocks
+// of first keys, then the blocks from `first` to the sequence's last.  Where nothing is
+// hidden between them (n - window <= sinks) the numbers are the sequence's own.  Hidden
+// rows are a block's last (the last sink block keeps sink_rows, the sequence's last block
+// the rows before n) or its first (block `first` hides `skip`), never both: a window of at
+// least one block does not end in the block it starts in unless it fills it.
+struct WindowBlocks {
+  int sink_blocks, sink_rows, first, skip, count;
+};
+constexpr int kMinWindow = kBlockSize;
+__host__ __device__ inline WindowBlocks window_blocks(int n, int window, int sinks) {
+  WindowBlocks w{0, 0, 0, 0, n / kBlockSize + (n % kBlockSize != 0)};
+  const int lo = n - window;
+  if (lo <= sinks) return w;
+  w.sink_blocks = sinks / kBlockSize + (sinks % kBlockSize != 0);
+  w.sink_rows = sinks - (w.sink_blocks - 1) * kBlockSize;
+  w.first = lo / kBlockSize;
+  w.skip = lo % kBlockSize;
+  w.count += w.sink_blocks - w.first;
+  return w;
+}
+// The sequence's block behind number v, and the rows [lo, hi) of it that are visible.
+__host__ __device__ inline int window_block(const WindowBlocks& w, int v) {
+  return v < w.sink_blocks ? v : w.first + v - w.sink_blocks;
+}
+__host__ __device__ inline void window_rows(const WindowBlocks& w, int n, int v, int* lo, int* hi) {
+  if (v < w.sink_blocks) {
+    *lo = 0;
+    *hi = v == w.sink_blocks - 1 ? w.sink_rows : kBlockSize;
+  } else {
+    const int left = n - window_block(w, v) * kBlockSize;
+    *lo = v == w.sink_blocks ? w.skip : 0;
+    *hi = left < kBlockSize ? left : kBlockSize;
+  }
 }
 
 __host__ __device__ inline int64_t meta_words(int B) {

@@ -55,6 +55,12 @@ struct Lengths {
   const int32_t* seqlens;
   const int32_t* q_lens;  // token schedule: per-sequence query counts, or null (rep each)
   int rep, causal;
+  int window, sinks;      // window > 0: only the blocks of visible keys count (window_blocks)
+  // blocks of a sequence of n keys
+  __device__ int blocks(int n) const {
+    if (n <= 0) return 0;
+    return window > 0 ? window_blocks(n, window, sinks).count : (n + kBlockSize - 1) / kBlockSize;
+  }
   __device__ int operator()(int b) const {
     if (rep == 0) return seqlens[b];
     const int r = b / rep;
@@ -89,8 +95,7 @@ __global__ void __launch_bounds__(kThreads) metadata_kernel(const Lengths len_of
   // one scan of the costs instead of two)
   if (B <= kThreads) {
     const int b = tid;
-    const int n = (b < B) ? len_of(b) : 0;
-    const int nb = n > 0 ? (n + kBlockSize - 1) / kBlockSize : 0;
+    const int nb = (b < B) ? len_of.blocks(len_of(b)) : 0;
     const int64_t nt = (nb + kBlocksPerTile - 1) / kBlocksPerTile;
     const int64_t cost = nb > 0 ? nt + kSchedOverheadTiles : 0;
     int64_t total;
@@ -150,6 +155,8 @@ __global__ void __launch_bounds__(kThreads) metadata_kernel(const Lengths len_of
       for (int i = kHdrOverhead + 1; i < kHdrWords; ++i) meta[i] = 0;
       meta[kHdrTokens] = len_of.rep;
       meta[kHdrTokCausal] = len_of.rep ? len_of.causal : 0;
+      meta[kHdrWindow] = len_of.window;
+      meta[kHdrSinks] = len_of.sinks;
     }
     return;
   }
@@ -160,8 +167,7 @@ __global__ void __launch_bounds__(kThreads) metadata_kernel(const Lengths len_of
     const int b = base + tid;
     int64_t cost = 0;
     if (b < B) {
-      const int n = len_of(b);
-      const int nb = n > 0 ? (n + kBlockSize - 1) / kBlockSize : 0;
+      const int nb = len_of.blocks(len_of(b));
       nblk_out[b] = nb;
       cost = nb > 0 ? (nb + kBlocksPerTile - 1) / kBlocksPerTile + kSchedOverheadTiles : 0;
     }
@@ -186,8 +192,7 @@ __global__ void __launch_bounds__(kThreads) metadata_kernel(const Lengths len_of
     int64_t cost = 0;
     int nb = 0;
     if (b < B) {
-      const int n = len_of(b);
-      nb = n > 0 ? (n + kBlockSize - 1) / kBlockSize : 0;
+      nb = len_of.blocks(len_of(b));
       cost = nb > 0 ? (nb + kBlocksPerTile - 1) / kBlocksPerTile + kSchedOverheadTiles : 0;
     }
     int64_t chunk_total;
@@ -258,14 +263,17 @@ __global__ void __launch_bounds__(kThreads) metadata_kernel(const Lengths len_of
     for (int i = kHdrOverhead + 1; i < kHdrWords; ++i) meta[i] = 0;
     meta[kHdrTokens] = len_of.rep;
     meta[kHdrTokCausal] = len_of.rep ? len_of.causal : 0;
+    meta[kHdrWindow] = len_of.window;
+    meta[kHdrSinks] = len_of.sinks;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_metadata(const int32_t* seqlens, int B, int s_q, int H, int num_workers,
-                            int32_t* meta, cudaStream_t stream, const int32_t* q_lens, int rep, int causal) {
-  const Lengths len_of{seqlens, q_lens, rep, causal};
+                            int32_t* meta, cudaStream_t stream, const int32_t* q_lens, int rep, int causal,
+                            int window, int sinks) {
+  const Lengths len_of{seqlens, q_lens, rep, causal, window, sinks};
   if (B <= 256)
     metadata_kernel<256><<<1, 256, 0, stream>>>(len_of, B, s_q, H, num_workers, meta);
   else

@@ -199,6 +199,36 @@ mla_status_t mla_decode_fp8_tokens(const void* q_nope, const void* q_pe, const v
                                    size_t workspace_bytes, void* out, float* lse, int32_t* status, void* stream);
 
 /*
+ * Decode attention with a sliding window and first keys that stay visible.  The token at
+ * position p sees the keys t <= p with t > p - window or t < sinks; everything else is
+ * mla_decode_tokens with the causal mask (tokens, positions, padding, q and out layout).
+ * The work is that of the visible keys: hidden blocks are neither scheduled nor read (their
+ * table entries may be stale), and hidden rows of the blocks at a window's edges never
+ * reach a result, whatever they hold.
+ *
+ *   window  >= 64 (smaller: MLA_ERR_UNSUPPORTED);  sinks >= 0
+ * mla_get_metadata_window: the schedule, for the same cache_seqlens, q_lens (NULL: s_q
+ *   each), window and sinks; mla_metadata_size(B * s_q, 1, H) bytes.
+ * mla_decode_window, mla_decode_fp8_window: over the bf16 and the packed FP8 cache; the
+ *   workspace holds mla_workspace_size(B * s_q, 1, H) bytes.  The split partials are merged
+ *   by the LSE combine as in mla_decode.  Device errors as in mla_decode_tokens (metadata
+ *   of another schedule, window or sinks: MLA_DEVICE_ERR_METADATA, and where that can be
+ *   told from the header alone nothing is written).
+ */
+mla_status_t mla_get_metadata_window(const int32_t* cache_seqlens, const int32_t* q_lens, int B, int s_q, int H,
+                                     int window, int sinks, void* metadata, size_t metadata_bytes, void* stream);
+mla_status_t mla_decode_window(const void* q_nope, const void* q_pe, const void* kv_cache, int64_t num_blocks,
+                               const int32_t* block_table, int max_blocks, const int32_t* cache_seqlens,
+                               const int32_t* q_lens, int B, int s_q, int H, float softmax_scale, int window,
+                               int sinks, const void* metadata, size_t metadata_bytes, void* workspace,
+                               size_t workspace_bytes, void* out, float* lse, int32_t* status, void* stream);
+mla_status_t mla_decode_fp8_window(const void* q_nope, const void* q_pe, const void* kv_fp8, int64_t num_blocks,
+                                   const int32_t* block_table, int max_blocks, const int32_t* cache_seqlens,
+                                   const int32_t* q_lens, int B, int s_q, int H, float softmax_scale, int window,
+                                   int sinks, const void* metadata, size_t metadata_bytes, void* workspace,
+                                   size_t workspace_bytes, void* out, float* lse, int32_t* status, void* stream);
+
+/*
  * The two launches mla_decode performs, exposed separately (same arguments, same
  * semantics; mla_decode == mla_decode_attention followed by mla_decode_combine on
  * the same stream with the same workspace).

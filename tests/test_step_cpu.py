@@ -173,3 +173,36 @@ def test_binding_refuses_wrong_tensors():
         mla.append_kv(torch.zeros(2, 1, 576, dtype=bf), torch.zeros(3, 64, 656, dtype=torch.uint8), table, n)
     with pytest.raises(ValueError, match="CUDA"):
         mla.append_kv(torch.zeros(2, 1, 576, dtype=bf), cache, table, n)
+
+
+# ---- windowed decode ------------------------------------------------------------------
+def window_args(**kw):
+    a = dict(q_nope=P, q_pe=P, cache=P, num_blocks=8, table=P, max_blocks=4, n=P, q_lens=None, B=2, s_q=2, H=16,
+             scale=0.1, window=64, sinks=0, meta=P, meta_bytes=1 << 30, ws=P, ws_bytes=1 << 40, out=P, lse=P,
+             status=None, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("code,kw", [
+    (1, dict(q_nope=None)), (1, dict(q_pe=None)), (1, dict(cache=None)), (1, dict(table=None)), (1, dict(n=None)),
+    (1, dict(meta=None)), (1, dict(out=None)), (1, dict(lse=None)), (1, dict(sinks=-1)), (1, dict(max_blocks=0)),
+    (1, dict(num_blocks=0)), (1, dict(scale=0.0)), (1, dict(scale=float("nan"))), (1, dict(q_lens=P + 2)),
+    (1, dict(out=P + 8)), (1, dict(lse=P + 1)), (1, dict(status=P + 1)),
+    (2, dict(window=63)), (2, dict(window=0)), (2, dict(window=-64)), (2, dict(H=48)), (2, dict(s_q=5)), (2, dict(B=0)),
+    (2, dict(B=40000, s_q=2)), (4, dict(meta_bytes=100)),
+])
+def test_window_refusals(code, kw):
+    for fn in ("mla_decode_window", "mla_decode_fp8_window"):
+        assert getattr(mla.load_library(), fn)(*window_args(**kw)) == code
+
+
+@pytest.mark.parametrize("code,kw", [
+    (1, dict(n=None)), (1, dict(meta=None)), (1, dict(meta=P + 4)), (1, dict(n=P + 2)), (1, dict(q_lens=P + 2)),
+    (1, dict(sinks=-1)), (2, dict(window=63)), (2, dict(s_q=5)), (2, dict(H=20)), (2, dict(B=65536, s_q=2)),
+    (4, dict(meta_bytes=16)),
+])
+def test_window_metadata_refusals(code, kw):
+    a = dict(n=P, q_lens=None, B=2, s_q=2, H=16, window=64, sinks=4, meta=P, meta_bytes=1 << 20, stream=None)
+    a.update(kw)
+    assert mla.load_library().mla_get_metadata_window(*a.values()) == code
