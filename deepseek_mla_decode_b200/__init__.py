@@ -13,6 +13,7 @@ missing or unbuildable library raises ``RuntimeError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -471,50 +472,82 @@ def rope_params(base: float = 10000.0, layout: str = "interleaved", scaling: str
     return r
 
 
-def _on_device(ref, named, stream):
-    """Checks the (name, tensor, dtype, shape) of `named` (None tensors are skipped; shape
-    None: any) against the CUDA device of `ref`, and returns the stream to launch on: the
-    given one, or that device's current one.  The device must be the current one."""
-    import torch
+_torch = None
 
-    dev = ref.device
-    if dev.type != "cuda":
+
+def _torch_module():
+    """torch, imported when the first tensor arrives (the library itself needs none)."""
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
+    return _torch
+
+
+# The calls of a decode step take 2-5 us on the device, so the checks below are kept to
+# attribute reads and tuple comparisons (about 0.3 us a tensor).
+def _expect(name, t, index, dtype, shape):
+    """t must be a contiguous tensor of dtype and shape (None: any) on CUDA device `index`."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _device_index(t):
+    """The CUDA device of t, which must be the current one."""
+    index = t.get_device()
+    if index < 0:
         raise ValueError("CUDA tensors expected")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t, dtype, shape in named:
-        if t is None:
-            continue
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if shape is not None and tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+    if index != _torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{index}, the current device is cuda:{_torch.cuda.current_device()}")
+    return index
+
+
+def _launch_stream(index, stream):
+    """The raw handle of `stream`, or of the device's current stream when it is None."""
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        return _torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
     return stream.cuda_stream
 
 
-def _token_rows(name, t, width):
-    """[B, s_q, ...] rows of `width` elements, contiguous in themselves and evenly spaced
-    (as a column slice of a fused projection is); returns (B, s_q, elements a row)."""
-    B, s_q = t.shape[:2]
-    inner, want = t.stride()[2:], []
-    step = 1
-    for d in reversed(t.shape[2:]):
-        want.insert(0, step)
-        step *= d
-    if any(s != w and d != 1 for s, w, d in zip(inner, want, t.shape[2:])):
+def _tokens(index, B, cache_seqlens, q_lens, status):
+    """Checks the per-sequence words of a call."""
+    i32 = _torch.int32
+    _expect("cache_seqlens", cache_seqlens, index, i32, (B,))
+    if q_lens is not None:
+        _expect("q_lens", q_lens, index, i32, (B,))
+    if status is not None:
+        _expect("status", status, index, i32, None)
+
+
+def _token_rows(name, t, inner, width):
+    """Elements between the consecutive tokens of t [B, s_q, ...], whose rows of `width`
+    elements are contiguous in themselves (strides `inner`) and evenly spaced, as a column
+    slice of a fused projection's output is."""
+    if t.is_contiguous():
+        return width
+    stride, (B, s_q) = t.stride(), t.shape[:2]
+    if stride[2:] != inner and any(a != b and d != 1 for a, b, d in zip(stride[2:], inner, t.shape[2:])):
         raise ValueError(f"{name}: the last dimensions must be contiguous")
-    row = t.stride(1) if s_q > 1 else (t.stride(0) if B > 1 else width)
-    if B > 1 and s_q > 1 and t.stride(0) != s_q * row:
+    if s_q == 1:
+        return stride[0] if B > 1 else width
+    if B > 1 and stride[0] != s_q * stride[1]:
         raise ValueError(f"{name}: the tokens must be evenly spaced (one row stride over [B, s_q])")
-    return B, s_q, row
+    return stride[1]
+
+
+@functools.lru_cache(maxsize=256)
+def _window_sizes(index, units, H):
+    """(schedule bytes, workspace bytes) of a token schedule over `units` on device `index`."""
+    return metadata_size(units, 1, H), workspace_size(units, 1, H)
 
 
 def _ptr(t):
@@ -525,60 +558,67 @@ def rope_q(q, cache_seqlens, rope: Rope, q_lens=None, q_heads=None, q_pe=None, s
     """mla_rope_q: splits query heads q [B, s_q, H, 192] = [128 | 64 rotary] into q_heads
     [B, s_q, H, 128] (for absorb_q) and q_pe [B, s_q, H, 64] (for decode), the latter rotated
     at each token's position.  q may be a column slice of a wider projection."""
-    import torch
-
-    if q.dim() != 4 or q.shape[3] != 192 or q.dtype != torch.bfloat16:
+    torch = _torch or _torch_module()
+    bf16 = torch.bfloat16
+    if q.dim() != 4 or q.shape[3] != 192 or q.dtype != bf16:
         raise ValueError("bf16 q [B, s_q, H, 192] expected")
-    H = q.shape[2]
-    B, s_q, row = _token_rows("q", q, H * 192)
+    B, s_q, H, _ = q.shape
+    row = _token_rows("q", q, (192, 1), H * 192)
+    index = _device_index(q)
+    _tokens(index, B, cache_seqlens, q_lens, status)
     if q_heads is None:
-        q_heads = torch.empty((B, s_q, H, 128), dtype=torch.bfloat16, device=q.device)
+        q_heads = q.new_empty((B, s_q, H, 128))
+    else:
+        _expect("q_heads", q_heads, index, bf16, (B, s_q, H, 128))
     if q_pe is None:
-        q_pe = torch.empty((B, s_q, H, 64), dtype=torch.bfloat16, device=q.device)
-    s = _on_device(q, (("cache_seqlens", cache_seqlens, torch.int32, (B,)), ("q_lens", q_lens, torch.int32, (B,)),
-                       ("q_heads", q_heads, torch.bfloat16, (B, s_q, H, 128)),
-                       ("q_pe", q_pe, torch.bfloat16, (B, s_q, H, 64)), ("status", status, torch.int32, None)), stream)
-    _check("mla_rope_q", load_library().mla_rope_q(
-        q.data_ptr(), row, cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, ctypes.byref(rope), q_heads.data_ptr(),
-        q_pe.data_ptr(), _ptr(status), s))
+        q_pe = q.new_empty((B, s_q, H, 64))
+    else:
+        _expect("q_pe", q_pe, index, bf16, (B, s_q, H, 64))
+    code = (_lib or load_library()).mla_rope_q(
+        q.data_ptr(), row, cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, rope, q_heads.data_ptr(),
+        q_pe.data_ptr(), _ptr(status), _launch_stream(index, stream))
+    if code:
+        raise MLAError("mla_rope_q", code)
     return q_heads, q_pe
 
 
 def rope_inplace(q, cache_seqlens, rope: Rope, q_lens=None, status=None, stream=None):
     """mla_rope_inplace: rotates the last 64 of each head of q [B, s_q, H, 192] where they
     lie; returns q."""
-    import torch
-
+    torch = _torch or _torch_module()
     if q.dim() != 4 or q.shape[3] != 192 or q.dtype != torch.bfloat16:
         raise ValueError("bf16 q [B, s_q, H, 192] expected")
-    H = q.shape[2]
-    B, s_q, row = _token_rows("q", q, H * 192)
-    s = _on_device(q, (("cache_seqlens", cache_seqlens, torch.int32, (B,)), ("q_lens", q_lens, torch.int32, (B,)),
-                       ("status", status, torch.int32, None)), stream)
-    _check("mla_rope_inplace", load_library().mla_rope_inplace(
-        q.data_ptr(), row, cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, ctypes.byref(rope), _ptr(status), s))
+    B, s_q, H, _ = q.shape
+    row = _token_rows("q", q, (192, 1), H * 192)
+    index = _device_index(q)
+    _tokens(index, B, cache_seqlens, q_lens, status)
+    _check("mla_rope_inplace", (_lib or load_library()).mla_rope_inplace(
+        q.data_ptr(), row, cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, rope, _ptr(status),
+        _launch_stream(index, stream)))
     return q
 
 
 def _append(fn, kv_a, cache, width, dtype, block_table, cache_seqlens, rope, norm_weight, eps, q_lens, status, stream):
-    import torch
-
-    if kv_a.dim() != 3 or kv_a.shape[2] != 576 or kv_a.dtype != torch.bfloat16:
+    if kv_a.dim() != 3 or kv_a.shape[2] != 576 or kv_a.dtype != _torch.bfloat16:
         raise ValueError("bf16 kv_a [B, s_q, 576] expected")
-    if cache.dim() != 3 or tuple(cache.shape[1:]) != (64, width):
+    if cache.dim() != 3 or cache.shape[1:] != (64, width):
         raise ValueError(f"cache [num_blocks, 64, {width}] expected")
     if block_table.dim() != 2:
         raise ValueError("block_table [B, max_blocks] expected")
-    B, s_q, row = _token_rows("kv_a", kv_a, 576)
-    s = _on_device(kv_a, (("cache", cache, dtype, None),
-                          ("block_table", block_table, torch.int32, (B, block_table.shape[1])),
-                          ("cache_seqlens", cache_seqlens, torch.int32, (B,)), ("q_lens", q_lens, torch.int32, (B,)),
-                          ("norm_weight", norm_weight, torch.bfloat16, (512,)), ("status", status, torch.int32, None)),
-                   stream)
-    _check(fn, getattr(load_library(), fn)(
-        kv_a.data_ptr(), row, _ptr(norm_weight), eps, block_table.data_ptr(), block_table.shape[1],
-        cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, ctypes.byref(rope) if rope is not None else None,
-        cache.data_ptr(), cache.shape[0], _ptr(status), s))
+    B, s_q, _ = kv_a.shape
+    row = _token_rows("kv_a", kv_a, (1,), 576)
+    index = _device_index(kv_a)
+    max_blocks = block_table.shape[1]
+    _tokens(index, B, cache_seqlens, q_lens, status)
+    _expect("cache", cache, index, dtype, None)
+    _expect("block_table", block_table, index, _torch.int32, (B, max_blocks))
+    if norm_weight is not None:
+        _expect("norm_weight", norm_weight, index, _torch.bfloat16, (512,))
+    code = getattr(_lib or load_library(), fn)(
+        kv_a.data_ptr(), row, _ptr(norm_weight), eps, block_table.data_ptr(), max_blocks, cache_seqlens.data_ptr(),
+        _ptr(q_lens), B, s_q, rope, cache.data_ptr(), cache.shape[0], _ptr(status), _launch_stream(index, stream))
+    if code:
+        raise MLAError(fn, code)
     return cache
 
 
@@ -587,8 +627,7 @@ def append_kv(kv_a, kv_cache, block_table, cache_seqlens, rope: Optional[Rope] =
     """mla_append_kv: writes the new tokens' rows kv_a [B, s_q, 576] = [c | k] into the paged
     bf16 cache [num_blocks, 64, 576]: c normalised by norm_weight (if given), k rotated by
     rope (if given).  cache_seqlens counts the new tokens.  Returns kv_cache."""
-    import torch
-
+    torch = _torch or _torch_module()
     return _append("mla_append_kv", kv_a, kv_cache, 576, torch.bfloat16, block_table, cache_seqlens, rope, norm_weight,
                    eps, q_lens, status, stream)
 
@@ -596,8 +635,7 @@ def append_kv(kv_a, kv_cache, block_table, cache_seqlens, rope: Optional[Rope] =
 def append_kv_fp8(kv_a, kv_fp8, block_table, cache_seqlens, rope: Optional[Rope] = None, norm_weight=None,
                   eps: float = 1e-6, q_lens=None, status=None, stream=None):
     """mla_append_kv_fp8: append_kv into the packed FP8 cache [num_blocks, 64, 656] (uint8)."""
-    import torch
-
+    torch = _torch or _torch_module()
     return _append("mla_append_kv_fp8", kv_a, kv_fp8, 656, torch.uint8, block_table, cache_seqlens, rope, norm_weight,
                    eps, q_lens, status, stream)
 
@@ -605,43 +643,54 @@ def append_kv_fp8(kv_a, kv_fp8, block_table, cache_seqlens, rope: Optional[Rope]
 def get_metadata_window(cache_seqlens, q_lens, s_q: int, H: int, window: int, sinks: int, metadata=None, stream=None):
     """mla_get_metadata_window: the schedule for decode_window / decode_fp8_window (shared by
     every layer of a step); q_lens may be None."""
-    import torch
-
-    B = cache_seqlens.shape[0]
+    torch = _torch or _torch_module()
+    (B,) = cache_seqlens.shape
+    index = _device_index(cache_seqlens)
+    _tokens(index, B, cache_seqlens, q_lens, None)
     if metadata is None:
-        metadata = torch.empty(metadata_size(B * s_q, 1, H) // 4, dtype=torch.int32, device=cache_seqlens.device)
-    s = _on_device(cache_seqlens, (("cache_seqlens", cache_seqlens, torch.int32, (B,)),
-                                   ("q_lens", q_lens, torch.int32, (B,)), ("metadata", metadata, torch.int32, None)),
-                   stream)
-    _check("mla_get_metadata_window", load_library().mla_get_metadata_window(
-        cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, window, sinks, metadata.data_ptr(), 4 * metadata.numel(), s))
+        metadata = cache_seqlens.new_empty(_window_sizes(index, B * s_q, H)[0] // 4)
+    else:
+        _expect("metadata", metadata, index, torch.int32, None)
+    _check("mla_get_metadata_window", (_lib or load_library()).mla_get_metadata_window(
+        cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, window, sinks, metadata.data_ptr(), 4 * metadata.numel(),
+        _launch_stream(index, stream)))
     return metadata
 
 
 def _decode_window(fn, q_nope, q_pe, kv, width, dtype, block_table, cache_seqlens, q_lens, softmax_scale, window, sinks,
                    metadata, workspace, out, lse, status, stream):
-    import torch
-
+    torch = _torch
     if q_nope.dim() != 4 or kv.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q_nope [B, s_q, H, 512], cache [num_blocks, 64, width], block_table [B, max_blocks] expected")
     B, s_q, H, _ = q_nope.shape
     bf16, i32 = torch.bfloat16, torch.int32
+    index = _device_index(q_nope)
+    max_blocks, num_blocks = block_table.shape[1], kv.shape[0]
+    _expect("q_nope", q_nope, index, bf16, (B, s_q, H, 512))
+    _expect("q_pe", q_pe, index, bf16, (B, s_q, H, 64))
+    _expect("cache", kv, index, dtype, (num_blocks, 64, width))
+    _expect("block_table", block_table, index, i32, (B, max_blocks))
+    _expect("metadata", metadata, index, i32, None)
+    _tokens(index, B, cache_seqlens, q_lens, status)
     if workspace is None:
-        workspace = torch.empty(workspace_size(B * s_q, 1, H), dtype=torch.uint8, device=q_nope.device)
+        workspace = kv.new_empty(_window_sizes(index, B * s_q, H)[1], dtype=torch.uint8)
+    else:
+        _expect("workspace", workspace, index, torch.uint8, None)
     if out is None:
-        out = torch.empty((B, s_q, H, 512), dtype=bf16, device=q_nope.device)
+        out = q_nope.new_empty((B, s_q, H, 512))
+    else:
+        _expect("out", out, index, bf16, (B, s_q, H, 512))
     if lse is None:
-        lse = torch.empty((B, s_q, H), dtype=torch.float32, device=q_nope.device)
-    s = _on_device(q_nope, (
-        ("q_nope", q_nope, bf16, (B, s_q, H, 512)), ("q_pe", q_pe, bf16, (B, s_q, H, 64)),
-        ("cache", kv, dtype, (kv.shape[0], 64, width)), ("block_table", block_table, i32, (B, block_table.shape[1])),
-        ("cache_seqlens", cache_seqlens, i32, (B,)), ("q_lens", q_lens, i32, (B,)), ("metadata", metadata, i32, None),
-        ("workspace", workspace, torch.uint8, None), ("out", out, bf16, (B, s_q, H, 512)),
-        ("lse", lse, torch.float32, (B, s_q, H)), ("status", status, i32, None)), stream)
-    _check(fn, getattr(load_library(), fn)(
-        q_nope.data_ptr(), q_pe.data_ptr(), kv.data_ptr(), kv.shape[0], block_table.data_ptr(), block_table.shape[1],
+        lse = q_nope.new_empty((B, s_q, H), dtype=torch.float32)
+    else:
+        _expect("lse", lse, index, torch.float32, (B, s_q, H))
+    code = getattr(_lib or load_library(), fn)(
+        q_nope.data_ptr(), q_pe.data_ptr(), kv.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks,
         cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, softmax_scale, window, sinks, metadata.data_ptr(),
-        4 * metadata.numel(), workspace.data_ptr(), workspace.numel(), out.data_ptr(), lse.data_ptr(), _ptr(status), s))
+        4 * metadata.numel(), workspace.data_ptr(), workspace.numel(), out.data_ptr(), lse.data_ptr(), _ptr(status),
+        _launch_stream(index, stream))
+    if code:
+        raise MLAError(fn, code)
     return out, lse
 
 
@@ -651,8 +700,7 @@ def decode_window(q_nope, q_pe, kv_cache, block_table, cache_seqlens, q_lens, so
     """mla_decode_window: decode_tokens in which the token at position p sees the keys
     t <= p with t > p - window or t < sinks (metadata from get_metadata_window with the same
     q_lens, window and sinks).  Returns (out bf16 [B, s_q, H, 512], lse fp32 [B, s_q, H])."""
-    import torch
-
+    torch = _torch or _torch_module()
     return _decode_window("mla_decode_window", q_nope, q_pe, kv_cache, 576, torch.bfloat16, block_table, cache_seqlens,
                           q_lens, softmax_scale, window, sinks, metadata, workspace, out, lse, status, stream)
 
@@ -661,8 +709,7 @@ def decode_fp8_window(q_nope, q_pe, kv_fp8, block_table, cache_seqlens, q_lens, 
                       sinks: int, metadata, workspace=None, out=None, lse=None, status=None,
                       stream=None) -> Tuple[object, object]:
     """mla_decode_fp8_window: decode_window over a packed FP8 cache [num_blocks, 64, 656]."""
-    import torch
-
+    torch = _torch or _torch_module()
     return _decode_window("mla_decode_fp8_window", q_nope, q_pe, kv_fp8, 656, torch.uint8, block_table, cache_seqlens,
                           q_lens, softmax_scale, window, sinks, metadata, workspace, out, lse, status, stream)
 
