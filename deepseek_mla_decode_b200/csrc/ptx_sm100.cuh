@@ -3,7 +3,7 @@
 // and the UMMA shared-memory / instruction descriptors.  The waits built on
 // mbar_try_wait are bounded by the caller (a %globaltimer deadline), so a protocol
 // bug turns into an error status instead of a hung GPU; the predicated TMA / MMA
-// issue forms live with the kernel that uses them.
+// issue forms of the CTA-pair kernels are in pair_ptx.cuh.
 #pragma once
 #include <cstdint>
 
@@ -158,6 +158,12 @@ __host__ __device__ constexpr uint32_t make_idesc_bf16(int M, int N, bool a_mn_m
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
          ((b_mn_major ? 1u : 0u) << 16) | ((static_cast<uint32_t>(N) >> 3) << 17) |
          ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
+// The same for kind::f8f6f4 with e4m3 A/B (format 0) and fp32 D.
+__host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
 }  // namespace ptx
