@@ -10,10 +10,11 @@
 //        2^-2 (2^-10 of the row's maximum) and off by at most 2^-10 below that.  k' splits
 //        the same way into [k'_hi | k'_lo], a fifth 128-wide chunk beside the four of codes,
 //        against [q_hi | q_hi] and [q_lo | q_lo].
-//   PV:  P = 2^(x + log2 s - m) (the row's scale rides in the exponent, m is the running
-//        maximum of x + log2 s, lazily) = P_hi + P_lo, kept in [0, 2^8.5], so the terms'
-//        smallest step is 2^-14.5 of the largest weight or finer; the normaliser
-//        l = sum 2^(x - m) = sum P / s is fp32.
+//   PV:  P = 2^(x - m) * f = P_hi + P_lo with f = s * scale * log2 e, the key's factor in
+//        its score x, too (the epilogue divides it out of the constant), and m the running
+//        maximum of x + log2 f, lazily: P stays in [0, 2^8.6] and the terms' smallest step
+//        is 2^-14 of the largest weight s 2^x or finer, whatever the scales are.  The
+//        normaliser l = sum 2^(x - m) is fp32.
 // Two 8-bit MMAs take the time of one bf16 MMA, so this costs no tensor time over the bf16
 // cache, moves half its bytes through the ring, and converts nothing but the 64 rotary
 // values a key.
@@ -58,8 +59,8 @@ constexpr int kSmemQ = 0;             // q_hi chunks 0..4, then q_lo chunks 0..4
 constexpr int kSmemP = kSmemQ + 2 * kChunks * kBoxBytes;  // P_hi (2 boxes of 128 keys), P_lo
 constexpr int kSmemRing = kSmemP + 4 * kBoxBytes;
 constexpr int kSmemRot = kSmemRing + kStages * kStageBytes;  // rotary keys' terms of this CTA's 128 keys
-constexpr int kSmemTab = kSmemRot + kStageBytes;             // two tables of 3 x 256 floats
-constexpr int kTabBytes = 3 * kTileKeys * 4;
+constexpr int kSmemTab = kSmemRot + kStageBytes;             // two tables of 256 floats
+constexpr int kTabBytes = kTileKeys * 4;
 constexpr int kSmemDyn = kSmemTab + 2 * kTabBytes;
 constexpr int kEpiRoundBytes = 4 * kBoxBytes;
 static_assert(4 * kEpiRoundBytes <= kSmemRot, "the last epilogue's staging stays inside Q, P and the ring");
@@ -67,12 +68,17 @@ static_assert(4 * kEpiRoundBytes <= kSmemRot, "the last epilogue's staging stays
 constexpr int kRegsIssue = 88, kRegsPrep = 88, kRegsSoftmax = 168;
 static_assert(128 * (kRegsIssue + kRegsPrep) + 256 * kRegsSoftmax == kThreads * 128, "register split");
 constexpr uint32_t kTmemO = 0, kTmemS0 = 256, kTmemCols = 512;
-// P <= 2^(kHeadroom + kRescaleThreshold) = 2^8.5 < 448.  More headroom makes small weights
-// finer, a larger threshold rescales O less often.
+// P <= 2^(kHeadroom + kRescaleThreshold + 0.086) < 2^8.6 < 448.  More headroom makes small
+// weights finer, a larger threshold rescales O less often.
 constexpr float kHeadroom = 5.0f, kRescaleThreshold = 3.5f;
-// Scales below this count as it in the exponent (a row of zeros has scale 0 but still
-// weighs 2^x in the normaliser; P / s stays in range).
-constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100
+constexpr float kBias = kHeadroom + 383.0f;  // the logarithm read off the bits is 383 high
+// Factors below this count as it: a row of zeros (scale 0) still weighs 2^x in the
+// normaliser, and 2^x is kept in units of the largest x + log2 factor.  With a query row's
+// power of two below 2^kMaxUp (rows under 2^-19 use fewer of their terms' bits; their scores
+// are near 0) the product of the two stays a normal number, so that a hidden key's -inf
+// stays one.
+constexpr float kMinFactor = 0x1p-96f;
+constexpr int kMaxUp = 26;
 constexpr uint32_t kIdescQK = make_idesc_e4m3(128, 256, false, false);
 constexpr uint32_t kIdescPV = make_idesc_e4m3(128, 256, false, true);
 constexpr int kBarSoftmax = 1, kBarPrep = 2;
@@ -258,36 +264,15 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
-// 64 bytes of a row, as keys 0..63: moved up by n keys, zeros in front
-__device__ __forceinline__ void keys_up(uint32_t (&w)[16], int n) {
-#pragma unroll
-  for (int i = 15; i >= 1; --i) w[i] = __funnelshift_l(w[i - 1], w[i], 8 * (n & 3));
-  w[0] <<= 8 * (n & 3);
-#pragma unroll
-  for (int bit = 0; bit < 4; ++bit) {
-    if ((n >> (2 + bit)) & 1) {
-#pragma unroll
-      for (int i = 15; i >= 0; --i) w[i] = (i >= (1 << bit)) ? w[i - (1 << bit)] : 0u;
-    }
-  }
-}
-// moved down by n keys, zeros behind
-__device__ __forceinline__ void keys_down(uint32_t (&w)[16], int n) {
-#pragma unroll
-  for (int i = 0; i < 15; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (n & 3));
-  w[15] >>= 8 * (n & 3);
-#pragma unroll
-  for (int bit = 0; bit < 4; ++bit) {
-    if ((n >> (2 + bit)) & 1) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = (i + (1 << bit) < 16) ? w[i + (1 << bit)] : 0u;
-    }
-  }
-}
-
 // Rows that no piece covers: no visible key (0 / -inf), an invalid length or count (NaN and
 // MLA_DEVICE_ERR_SEQLEN), a stale block count (NaN and MLA_DEVICE_ERR_METADATA).  Partition
 // `part` takes the units b with b % P == part; a warp writes this CTA's rows from y0 on.
@@ -727,15 +712,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = wait_bar(&ctrl, p, smem_u32(&ctrl.s_full[buf]), (qk_count >> 1) & 1) && ok;
           if (t == 0) rs = ctrl.row_scale[npieces & 3][m];
           tc_fence_after();
-          uint32_t sr[64];
-          {
-            uint32_t (&a)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
-            uint32_t (&b)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
-            const uint32_t ta = tmem + kTmemS0 + 128 * buf + lane_off + 64 * g;
-            tmem_ld32(ta, a);
-            tmem_ld32(ta + 32, b);
-            tmem_wait_ld();
-          }
+          const uint32_t ts = tmem + kTmemS0 + 128 * buf + lane_off + 64 * g;
           // of this thread's block, keys [c0, c0 + cnt) are visible
           int c0 = 0, hi = kBlockSize, cnt = 0;
           if (2 * hk + g < blocks_in_tile(pc, t)) {
@@ -744,26 +721,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           auto seen = [&](int c) -> bool { return (uint32_t)(c - c0) < (uint32_t)cnt; };
           const bool full = __all_sync(0xffffffffu, cnt == kBlockSize);
-          // y = x + log2 s, x = S * scale_key * scale * log2 e * 2^-j
+          // x = S * 2^-j * f with the key's factor f = s * scale * log2 e; the maximum is of
+          // x + log2 f, the logarithm read off the factor's bits (exponent and mantissa as a
+          // fixed-point number: at most 0.087 below it)
           const float4* tab = reinterpret_cast<const float4*>(smem + kSmemTab + buf * kTabBytes) + 16 * (2 * hk + g);
-          float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+          uint32_t sr[32];
+          // scores of the 32 keys from c on (hidden ones -inf, whose weight 2^-inf is 0)
+          auto load_scores = [&](int c) {
+            tmem_ld32(ts + c, sr);
+            tmem_wait_ld();
+            if (!full) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            const float4 k = tab[c >> 2], l = tab[64 + (c >> 2)];
-            const float y0_ = fmaf(__uint_as_float(sr[c]) * k.x, rs, l.x);
-            const float y1_ = fmaf(__uint_as_float(sr[c + 1]) * k.y, rs, l.y);
-            const float y2_ = fmaf(__uint_as_float(sr[c + 2]) * k.z, rs, l.z);
-            const float y3_ = fmaf(__uint_as_float(sr[c + 3]) * k.w, rs, l.w);
-            if (full || seen(c)) mx0 = fmaxf(mx0, y0_);
-            if (full || seen(c + 1)) mx1 = fmaxf(mx1, y1_);
-            if (full || seen(c + 2)) mx2 = fmaxf(mx2, y2_);
-            if (full || seen(c + 3)) mx3 = fmaxf(mx3, y3_);
-            sr[c] = __float_as_uint(y0_);
-            sr[c + 1] = __float_as_uint(y1_);
-            sr[c + 2] = __float_as_uint(y2_);
-            sr[c + 3] = __float_as_uint(y3_);
+              for (int i = 0; i < 32; ++i)
+                if (!seen(c + i)) sr[i] = 0xff800000u;
+            }
+          };
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            load_scores(c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 f = tab[(c + i) >> 2];
+              const float k[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // 2^23 + the factor's upper 23 bits, as a float: log2 in steps of 2^-15, 383 high
+                const float lg = __uint_as_float(__byte_perm(__float_as_uint(k[e]), 0x4B000000u, 0x7321));
+                mx[e] = fmaxf(mx[e], fmaf(lg, 0x1p-15f, __uint_as_float(sr[i + e]) * (k[e] * rs)));
+              }
+            }
           }
-          ctrl.red_max[buf][2 * hk + g][m] = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+          ctrl.red_max[buf][2 * hk + g][m] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           go = named_bar_and(kBarSoftmax, kNumSoftmaxThreads, ok);
           if (!go) break;
           const float m_new =
@@ -776,21 +765,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             m_used = m_new;
             l_part *= alpha;
           }
-          const float nref = (m_used == -INFINITY) ? 0.f : kHeadroom - m_used;
-          uint32_t ph[16], pl[16];
-          float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            const float4 inv = tab[128 + (c >> 2)];
-            const float p0 = (full || seen(c)) ? fast_exp2(__uint_as_float(sr[c]) + nref) : 0.f;
-            const float p1 = (full || seen(c + 1)) ? fast_exp2(__uint_as_float(sr[c + 1]) + nref) : 0.f;
-            const float p2 = (full || seen(c + 2)) ? fast_exp2(__uint_as_float(sr[c + 2]) + nref) : 0.f;
-            const float p3 = (full || seen(c + 3)) ? fast_exp2(__uint_as_float(sr[c + 3]) + nref) : 0.f;
-            l0 = fmaf(p1, inv.y, fmaf(p0, inv.x, l0));
-            l1 = fmaf(p3, inv.w, fmaf(p2, inv.z, l1));
-            split4(p0, p1, p2, p3, ph[c >> 2], pl[c >> 2]);
-          }
-          l_part += l0 + l1;
+          const float nref = (m_used == -INFINITY) ? 0.f : kBias - m_used;
           // PV of the previous tile (possibly the previous piece's last) must be done before
           // P is overwritten, O is rescaled or the previous piece's O is read
           if (qk_count >= 1) {
@@ -825,25 +800,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tmem_wait_st();
             }
           }
-          // the block's keys sit where its V rows were loaded (warp-uniform)
-          if (hi < kBlockSize) {
-            keys_up(ph, kBlockSize - hi);
-            keys_up(pl, kBlockSize - hi);
-          } else if (c0 > 0) {
-            keys_down(ph, c0);
-            keys_down(pl, c0);
-          }
-          // P -> shared memory: K-major, box hk holds keys 128hk.. of all 64 rows, this
-          // thread's 64 keys are granules 4g..4g+3 of its row (granule j at j ^ (m & 7))
-          {
-            const uint32_t prow = sP + hk * kBoxBytes + m * 128;
+          // P -> shared memory: K-major, box hk holds keys 128hk.. of all 64 rows, this thread's
+          // 64 keys are granules 4g..4g+3 of its row (granule j at j ^ (m & 7)).  A block with
+          // hidden rows has its keys where its V rows were loaded, 64 - hi further on or c0
+          // further back: as a rotation, for the hidden keys' zeros belong where these leave.
+          float l0 = 0.f, l1 = 0.f;
+          const uint32_t prow = sP + hk * kBoxBytes + m * 128;
+          const int turn = hi < kBlockSize ? kBlockSize - hi : kBlockSize - c0;  // 64: none
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            load_scores(c);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t a = prow + (((4 * g + j) ^ (m & 7)) << 4);
-              st_shared_v4(a, ph[4 * j], ph[4 * j + 1], ph[4 * j + 2], ph[4 * j + 3]);
-              st_shared_v4(a + 2 * kBoxBytes, pl[4 * j], pl[4 * j + 1], pl[4 * j + 2], pl[4 * j + 3]);
+            for (int j = 0; j < 2; ++j) {
+              uint32_t ph[4], pl[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float4 f = tab[(c >> 2) + 4 * j + q];
+                const uint32_t* x = &sr[16 * j + 4 * q];
+                const float e0 = fast_exp2(fmaf(__uint_as_float(x[0]), f.x * rs, nref));
+                const float e1 = fast_exp2(fmaf(__uint_as_float(x[1]), f.y * rs, nref));
+                const float e2 = fast_exp2(fmaf(__uint_as_float(x[2]), f.z * rs, nref));
+                const float e3 = fast_exp2(fmaf(__uint_as_float(x[3]), f.w * rs, nref));
+                l0 += e0 + e1;
+                l1 += e2 + e3;
+                split4(e0 * f.x, e1 * f.y, e2 * f.z, e3 * f.w, ph[q], pl[q]);
+              }
+              if (turn == kBlockSize) {  // warp-uniform
+                const uint32_t a = prow + (((4 * g + (c >> 4) + j) ^ (m & 7)) << 4);
+                st_shared_v4(a, ph[0], ph[1], ph[2], ph[3]);
+                st_shared_v4(a + 2 * kBoxBytes, pl[0], pl[1], pl[2], pl[3]);
+              } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+#pragma unroll 1
+                  for (int e = 0; e < 4; ++e) {
+                    const int k = (c + 16 * j + 4 * q + e + turn) & 63;
+                    const uint32_t a = prow + (((4 * g + (k >> 4)) ^ (m & 7)) << 4) + (k & 15);
+                    st_shared_u8(a, ph[q] >> (8 * e));
+                    st_shared_u8(a + 2 * kBoxBytes, pl[q] >> (8 * e));
+                  }
+                }
+              }
             }
           }
+          l_part += l0 + l1;
           fence_proxy_async_smem();
           tc_fence_before();
           named_bar_sync(kBarSoftmax, kNumSoftmaxThreads);
@@ -868,10 +868,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool bad = ctrl.bad_piece != 0;
         const float nanf_ = __int_as_float(0x7fc00000);
         // NaN scales make the row NaN; so does a NaN among the visible scores (l is NaN then)
-        pend_sc = (bad || l_row != l_row) ? nanf_ : ((l_row > 0.f) ? 1.f / l_row : 0.f);
+        // (the factors in P carry scale * log2 e beside s)
+        pend_sc = (bad || l_row != l_row) ? nanf_ : ((l_row > 0.f) ? 1.f / (l_row * p.scale_log2) : 0.f);
         pend_lse = (bad || l_row != l_row)
                        ? nanf_
-                       : ((l_row > 0.f) ? (m_used - kHeadroom + __log2f(l_row)) * 0.69314718055994531f : -INFINITY);
+                       : ((l_row > 0.f) ? (m_used - kBias + __log2f(l_row)) * 0.69314718055994531f : -INFINITY);
         pend_direct = (nsplit == 1);
         pend_b = pc.b;
         pend_slot = split_base + pc.split;
@@ -910,7 +911,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       // ---- query rows: warp pw takes rows 16pw.. of this CTA, four at a time; lane l holds
       // values 16l.. of q_nope (granule l % 8 of chunk l / 8) and 2l.. of q_pe
-      constexpr int kBatch = 4;
+      constexpr int kBatch = 2;
       uint4 qa[kBatch], qb[kBatch];
       uint32_t qr[kBatch];
       auto load_rows = [&](int b, int r0) {
@@ -938,7 +939,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, w[k] & 0x7fff7fffu);
           mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
           const int E = (int)(mx >> 7);  // biased exponent of the row's largest value
-          const int j = min(134 - E, 126);
+          const int j = min(134 - E, kMaxUp);
           const float up = __int_as_float((j + 127) << 23);
           if (lane == 0)
             ctrl.row_scale[piece & 3][m] = E == 255 ? __int_as_float(0x7fc00000) : __int_as_float((127 - j) << 23);
@@ -961,47 +962,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           st_shared_u16(row + kChunks * kBoxBytes + g1, rl);
         }
       };
-      // ---- a tile: thread pt holds this CTA's key pt (its rotary part) and the scales of
-      // the tile's keys pt and 128 + pt
-      uint4 raw[8];
+      // ---- a tile: thread pt holds the scales of the tile's keys pt and 128 + pt; warp pw
+      // takes the rotary parts of this CTA's keys 32pw.., eight lanes a row
+      const uint8_t* own = nullptr;  // the first of this lane's rotary pieces
       float sA = 0.f, sB = 0.f;
       const int r = pt & 63;
+      bool seenA = false, seenB = false;  // whether those two keys are visible
       auto load_tile = [&](const Piece& pc, const int32_t* bt, int t) {
         const int nb = blocks_in_tile(pc, t), v0 = pc.k_lo + t * kBlocksPerTile, kb = pt >> 6;
-        const uint8_t *rowA = nullptr, *rowB = nullptr;
+        const uint8_t *blkA = nullptr, *blkB = nullptr;
+        seenA = seenB = false;
         if (kb < nb) {
           const int32_t id = bt[window_block(pc.w, v0 + kb)];
-          rowA = p.rows + ((int64_t)(valid_id(p, id) ? id : 0) * kBlockSize + r) * kRowBytes8;
+          blkA = p.rows + (int64_t)(valid_id(p, id) ? id : 0) * (kBlockSize * kRowBytes8);
+          int lo, hi;
+          rows_in_block(pc, t, kb, &lo, &hi);
+          seenA = r >= lo && r < hi;
         }
         if (kb + 2 < nb) {
           const int32_t id = bt[window_block(pc.w, v0 + kb + 2)];
-          rowB = p.rows + ((int64_t)(valid_id(p, id) ? id : 0) * kBlockSize + r) * kRowBytes8;
+          blkB = p.rows + (int64_t)(valid_id(p, id) ? id : 0) * (kBlockSize * kRowBytes8);
+          int lo, hi;
+          rows_in_block(pc, t, kb + 2, &lo, &hi);
+          seenB = r >= lo && r < hi;
         }
-        sA = rowA ? __ldg(reinterpret_cast<const float*>(rowA + kOffScale8)) : 0.f;
-        sB = rowB ? __ldg(reinterpret_cast<const float*>(rowB + kOffScale8)) : 0.f;
-        const uint8_t* own = leader ? rowA : rowB;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          raw[k] = own ? __ldg(reinterpret_cast<const uint4*>(own + kOffKpe8) + k) : make_uint4(0u, 0u, 0u, 0u);
+        sA = blkA ? __ldg(reinterpret_cast<const float*>(blkA + r * kRowBytes8 + kOffScale8)) : 0.f;
+        sB = blkB ? __ldg(reinterpret_cast<const float*>(blkB + r * kRowBytes8 + kOffScale8)) : 0.f;
+        own = leader ? blkA : blkB;
+        if (own) own += (32 * (pw & 1) + (lane >> 3)) * kRowBytes8 + kOffKpe8 + 16 * (lane & 7);
       };
-      auto table_entry = [&](float* tab, int key, float s) {
-        const float se = fmaxf(s, kMinScale);
-        tab[key] = s * p.scale_log2;
-        tab[kTileKeys + key] = log2f(se);
-        tab[2 * kTileKeys + key] = __frcp_rn(se);
+      auto table_entry = [&](float* tab, int key, float s, bool seen) {
+        float f = seen ? s * p.scale_log2 : 1.0f;  // a hidden key's scale may be anything
+        if (f < kMinFactor) f = kMinFactor;        // a NaN stays
+        tab[key] = f;
       };
       auto store_rotary = [&]() {
-        const uint32_t row = sRot + (pt >> 6) * kBoxBytes + r * 128;
+        // this lane's 8 values of a row: half (lane & 1) of granule (lane % 8) / 2 of the hi
+        // terms, and of granule 4 + (lane % 8) / 2 of the lo terms
+        const int j = lane & 7;
+#pragma unroll 1
+        for (int k0 = 0; k0 < 8; k0 += 2) {
+          uint4 raw[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // 16 values: granule k of the hi half, 4 + k of the lo half
-          const uint32_t w[8] = {raw[2 * k].x,     raw[2 * k].y,     raw[2 * k].z,     raw[2 * k].w,
-                                 raw[2 * k + 1].x, raw[2 * k + 1].y, raw[2 * k + 1].z, raw[2 * k + 1].w};
-          uint32_t h[4], l[4];
+          for (int k = 0; k < 2; ++k)
+            raw[k] = own ? __ldg(reinterpret_cast<const uint4*>(own + 4 * (k0 + k) * kRowBytes8))
+                         : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            split4(bf_lo(w[2 * q]), bf_hi(w[2 * q]), bf_lo(w[2 * q + 1]), bf_hi(w[2 * q + 1]), h[q], l[q]);
-          st_shared_v4(row + ((k ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-          st_shared_v4(row + (((4 + k) ^ (r & 7)) << 4), l[0], l[1], l[2], l[3]);
+          for (int k = 0; k < 2; ++k) {
+            const int m = 32 * (pw & 1) + 4 * (k0 + k) + (lane >> 3);
+            uint32_t h0, l0, h1, l1;
+            split4(bf_lo(raw[k].x), bf_hi(raw[k].x), bf_lo(raw[k].y), bf_hi(raw[k].y), h0, l0);
+            split4(bf_lo(raw[k].z), bf_hi(raw[k].z), bf_lo(raw[k].w), bf_hi(raw[k].w), h1, l1);
+            const uint32_t row = sRot + (pw >> 1) * kBoxBytes + m * 128 + 8 * (j & 1);
+            st_shared_v2(row + (((j >> 1) ^ (m & 7)) << 4), h0, h1);
+            st_shared_v2(row + (((4 + (j >> 1)) ^ (m & 7)) << 4), l0, l1);
+          }
         }
       };
       Walker walk(p, part);
@@ -1040,8 +1055,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (tiles >= 1) ok = wait_bar(&ctrl, p, smem_u32(&ctrl.k_empty), (tiles - 1) & 1) && ok;
           if (ok) {
             float* tab = tables + buf * (kTabBytes / 4);
-            table_entry(tab, pt, sA);
-            table_entry(tab, 128 + pt, sB);
+            table_entry(tab, pt, sA, seenA);
+            table_entry(tab, 128 + pt, sB, seenB);
             store_rotary();
           }
           if (!publish()) break;
