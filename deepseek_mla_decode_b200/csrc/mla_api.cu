@@ -23,9 +23,9 @@ cudaError_t launch_combine(const int32_t* meta, const int32_t* seqlens, const in
                            int sinks = 0);
 cudaError_t decode_kernel_setup(int device);
 cudaError_t window_fp8_setup();
-cudaError_t launch_window_fp8(const CUtensorMap& tm_rows, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
-                              const void* rows, const void* q_nope, const void* q_pe, const int32_t* block_table,
-                              int max_blocks, const int32_t* seqlens, const int32_t* q_lens, const int32_t* meta,
+cudaError_t launch_window_fp8(const CUtensorMap& tm_rows, const CUtensorMap& tm_qn, const CUtensorMap& tm_qp,
+                              const CUtensorMap& tm_out, const CUtensorMap& tm_part, const void* rows,
+                              const int32_t* block_table, int max_blocks, const int32_t* seqlens, const int32_t* q_lens, const int32_t* meta,
                               int64_t num_blocks, int units, int rep, int H, float scale, int window, int sinks,
                               void* out, float* lse, float* part_lse, int32_t* status, int num_ctas,
                               uint64_t wait_timeout_ns, int inject_stall, cudaStream_t stream);
@@ -285,6 +285,20 @@ mla_status_t launch_attention(bool fp8, const void* q_nope, const void* q_pe, co
                               float* lse, int32_t* status, const DecodeGeom& g, cudaStream_t s, int tok_rep = 0,
                               int tok_causal = 0, const int32_t* tok_q_lens = nullptr, int window = 0,
                               int sinks = 0) {
+  const int64_t rows = static_cast<int64_t>(B) * g.M;
+  CUtensorMap tm_qn, tm_qp;
+  {
+    cuuint64_t dims[2] = {(cuuint64_t)mla::kDLatent, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)mla::kDLatent * 2};
+    cuuint32_t box[2] = {64, 64};
+    if (!encode(&tm_qn, q_nope, 2, dims, strides, box)) return MLA_ERR_INVALID_ARG;
+  }
+  {
+    cuuint64_t dims[2] = {(cuuint64_t)mla::kDRope, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)mla::kDRope * 2};
+    cuuint32_t box[2] = {64, 64};
+    if (!encode(&tm_qp, q_pe, 2, dims, strides, box)) return MLA_ERR_INVALID_ARG;
+  }
   float* part_o = static_cast<float*>(workspace);
   float* part_lse = part_o + g.slots * g.M * mla::kDLatent;
   // Output views for the epilogue's TMA stores: rows past M of a sequence are clipped.
@@ -310,15 +324,14 @@ mla_status_t launch_attention(bool fp8, const void* q_nope, const void* q_pe, co
     cuuint32_t box[3] = {128, (cuuint32_t)mla::kBlockSize, 1};
     if (!encode(&tm_rows, kv_cache, 3, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B))
       return MLA_ERR_INVALID_ARG;
-    if (mla::launch_window_fp8(tm_rows, tm_out, tm_part, kv_cache, q_nope, q_pe, block_table, max_blocks,
+    if (mla::launch_window_fp8(tm_rows, tm_qn, tm_qp, tm_out, tm_part, kv_cache, block_table, max_blocks,
                                cache_seqlens, tok_q_lens, static_cast<const int32_t*>(metadata), num_blocks, B,
                                tok_rep, H, softmax_scale, window, sinks, out, lse, part_lse, status, 2 * g.P * g.T,
                                g_wait_timeout_ns.load(), g_inject_stall.load(), s) != cudaSuccess)
       return MLA_ERR_CUDA;
     return MLA_OK;
   }
-  const int64_t rows = static_cast<int64_t>(B) * g.M;
-  CUtensorMap tm_kv, tm_kv2, tm_qn, tm_qp, tm_kpe, tm_scl;
+  CUtensorMap tm_kv, tm_kv2, tm_kpe, tm_scl;
   if (fp8) {
     if (!encode_fp8_cache(kv_cache, num_blocks, &tm_kv, &tm_kv2, &tm_kpe, &tm_scl)) return MLA_ERR_INVALID_ARG;
   } else {
@@ -337,18 +350,6 @@ mla_status_t launch_attention(bool fp8, const void* q_nope, const void* q_pe, co
     cuuint32_t box[4] = {64, 64, 2, 1};
     if (!encode(&tm_kv2, kv_cache, 4, dims, strides, box)) return MLA_ERR_INVALID_ARG;
     }
-  }
-  {
-    cuuint64_t dims[2] = {(cuuint64_t)mla::kDLatent, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)mla::kDLatent * 2};
-    cuuint32_t box[2] = {64, 64};
-    if (!encode(&tm_qn, q_nope, 2, dims, strides, box)) return MLA_ERR_INVALID_ARG;
-  }
-  {
-    cuuint64_t dims[2] = {(cuuint64_t)mla::kDRope, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)mla::kDRope * 2};
-    cuuint32_t box[2] = {64, 64};
-    if (!encode(&tm_qp, q_pe, 2, dims, strides, box)) return MLA_ERR_INVALID_ARG;
   }
   if (mla::launch_decode(fp8, tm_kv, tm_kv2, fp8 ? &tm_kpe : nullptr, fp8 ? &tm_scl : nullptr, tm_qn, tm_qp,
                          tm_out, tm_part, block_table, max_blocks, cache_seqlens,

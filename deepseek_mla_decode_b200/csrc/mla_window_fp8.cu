@@ -55,12 +55,12 @@ constexpr int kBoxBytes = 8192;       // 64 rows x 128 bytes, 128-byte swizzle
 constexpr int kStageBytes = 2 * kBoxBytes;
 constexpr int kCodeChunks = 4;        // 512 codes / 128
 constexpr int kChunks = kCodeChunks + 1;  // and the rotary one
-constexpr int kSmemQ = 0;             // q_hi chunks 0..4, then q_lo chunks 0..4
+constexpr int kSmemQ = 0;             // box 2c: q_hi of chunk c, box 2c + 1: q_lo
 constexpr int kSmemP = kSmemQ + 2 * kChunks * kBoxBytes;  // P_hi (2 boxes of 128 keys), P_lo
 constexpr int kSmemRing = kSmemP + 4 * kBoxBytes;
 constexpr int kSmemRot = kSmemRing + kStages * kStageBytes;  // rotary keys' terms of this CTA's 128 keys
-constexpr int kSmemTab = kSmemRot + kStageBytes;             // two tables of 256 floats
-constexpr int kTabBytes = kTileKeys * 4;
+constexpr int kSmemTab = kSmemRot + kStageBytes;             // two tables of 2 x 256 floats
+constexpr int kTabBytes = 2 * kTileKeys * 4;
 constexpr int kSmemDyn = kSmemTab + 2 * kTabBytes;
 constexpr int kEpiRoundBytes = 4 * kBoxBytes;
 static_assert(4 * kEpiRoundBytes <= kSmemRot, "the last epilogue's staging stays inside Q, P and the ring");
@@ -71,14 +71,12 @@ constexpr uint32_t kTmemO = 0, kTmemS0 = 256, kTmemCols = 512;
 // P <= 2^(kHeadroom + kRescaleThreshold + 0.086) < 2^8.6 < 448.  More headroom makes small
 // weights finer, a larger threshold rescales O less often.
 constexpr float kHeadroom = 5.0f, kRescaleThreshold = 3.5f;
+constexpr float kLogUnit = 0x1p15f;
 constexpr float kBias = kHeadroom + 383.0f;  // the logarithm read off the bits is 383 high
 // Factors below this count as it: a row of zeros (scale 0) still weighs 2^x in the
-// normaliser, and 2^x is kept in units of the largest x + log2 factor.  With a query row's
-// power of two below 2^kMaxUp (rows under 2^-19 use fewer of their terms' bits; their scores
-// are near 0) the product of the two stays a normal number, so that a hidden key's -inf
-// stays one.
-constexpr float kMinFactor = 0x1p-96f;
-constexpr int kMaxUp = 26;
+// normaliser, and 2^x is kept in units of the largest x + log2 factor.
+constexpr float kMinFactor = 0x1p-100f;
+constexpr int kMaxUp = 100;  // largest power of two of a query row
 constexpr uint32_t kIdescQK = make_idesc_e4m3(128, 256, false, false);
 constexpr uint32_t kIdescPV = make_idesc_e4m3(128, 256, false, true);
 constexpr int kBarSoftmax = 1, kBarPrep = 2;
@@ -87,11 +85,11 @@ constexpr uint64_t kQuiesceNs = 500000ull;       // post-abort wait for TMA load
 
 struct Params {
   CUtensorMap tm_rows;  // packed rows as bytes [num_blocks][64][656], box {128, 64, 1}, SW128
+  CUtensorMap tm_qn;    // q_nope as [units * M][512] bf16, box {64, 64}, SW128
+  CUtensorMap tm_qp;    // q_pe as [units * M][64] bf16, box {64, 64}, SW128
   CUtensorMap tm_out;   // out as [units][M][512] bf16, box {64, 64, 1}, SW128 (TMA store)
   CUtensorMap tm_part;  // partial outputs as [slots][M][512] fp32, box {32, 64, 1}, SW128
   const uint8_t* rows;
-  const __nv_bfloat16* q_nope;
-  const __nv_bfloat16* q_pe;
   const int32_t* block_table;
   const int32_t* seqlens;
   const int32_t* q_lens;
@@ -114,6 +112,8 @@ struct __align__(8) Ctrl {
   uint64_t empty[kStages];  // both: stage consumed by the MMAs (commit)
   uint64_t q_full;          // leader: both CTAs' query terms written (count 2)
   uint64_t q_empty;         // both: last QK of the piece done (commit)
+  uint64_t q_raw;           // this CTA's query rows landed as bf16 (count 1 + tx)
+  uint64_t k_raw;           // this CTA's rotary keys landed as bf16 (count 1 + tx)
   uint64_t k_full;          // leader: both CTAs' rotary keys written (count 2)
   uint64_t k_empty;         // both: rotary QK of the tile done (commit)
   uint64_t sc_full[2];      // scale table of a tile written (count 1)
@@ -238,31 +238,65 @@ __device__ __forceinline__ bool wait_bar(Ctrl* c, const Params& p, uint32_t bar,
 }
 
 
-// p0, p1 -> two e4m3 terms each: hi the rounded values, lo what that left, both as pairs.
-// fp16 carries P's 11 bits and the remainder exactly.
-__device__ __forceinline__ void split_e4m3x2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
-  asm("{\n\t.reg .b32 h, b, r;\n\t.reg .b16 e, f;\n\t"
-      "cvt.rn.f16x2.f32 h, %3, %2;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 e, h;\n\t"
-      "cvt.rn.f16x2.e4m3x2 b, e;\n\t"
-      "sub.rn.f16x2 r, h, b;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 f, r;\n\t"
-      "cvt.u32.u16 %0, e;\n\tcvt.u32.u16 %1, f;\n\t}"
-      : "=r"(hi), "=r"(lo)
-      : "f"(p0), "f"(p1));
+// Four values as two e4m3 terms each: hi the value rounded to e4m3's four bits (an fp32 add
+// and mask: ties away, above the smallest normal), lo what that left.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 x, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\t"
+      "mov.b32 %0, {x, y};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
-// four values -> a word of hi and a word of lo terms
+__device__ __forceinline__ float top4(float x) {
+  return __int_as_float((__float_as_int(x) + 0x80000) & 0xfff00000);
+}
 __device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
-  uint32_t h0, l0, h1, l1;
-  split_e4m3x2(a, b, h0, l0);
-  split_e4m3x2(c, d, h1, l1);
-  hi = __byte_perm(h0, h1, 0x5410);
-  lo = __byte_perm(l0, l1, 0x5410);
+  const float ta = top4(a), tb = top4(b), tc = top4(c), td = top4(d);
+  hi = e4m3x4(ta, tb, tc, td);
+  lo = e4m3x4(a - ta, b - tb, c - tc, d - td);
+}
+// packed pairs of fp32
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t* w) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t w;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(addr) : "memory");
+  return w;
 }
 __device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
@@ -319,6 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&ctrl.q_full), 2);
     mbar_init(smem_u32(&ctrl.q_empty), 1);
+    mbar_init(smem_u32(&ctrl.q_raw), 1);
+    mbar_init(smem_u32(&ctrl.k_raw), 1);
     mbar_init(smem_u32(&ctrl.k_full), 2);
     mbar_init(smem_u32(&ctrl.k_empty), 1);
     for (int s = 0; s < 2; ++s) {
@@ -344,6 +380,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&p.tm_rows);
+    prefetch_tmap(&p.tm_qn);
+    prefetch_tmap(&p.tm_qp);
     prefetch_tmap(&p.tm_out);
     prefetch_tmap(&p.tm_part);
   }
@@ -505,11 +543,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       };
       auto mma_chunk = [&](uint32_t d, int c, uint64_t b0) {
-        const uint64_t a0 = dq0 + c * kBoxD;
+        const uint64_t a0 = dq0 + 2 * c * kBoxD;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           umma8_2sm_if(elected, d, a0 + 2 * ks, b0 + 2 * ks, kIdescQK, (c | ks) != 0);
-          umma8_2sm_if(elected, d, a0 + kChunks * kBoxD + 2 * ks, b0 + 2 * ks, kIdescQK, 1);
+          umma8_2sm_if(elected, d, a0 + kBoxD + 2 * ks, b0 + 2 * ks, kIdescQK, 1);
         }
       };
       auto mma_qk = [&](int nt, int t) {
@@ -638,16 +676,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               uint32_t o[32];
-              tmem_ld32(to + 64 * r + 32 * hf, o);
-              tmem_wait_ld();
+              tmem_ld32_wait(to + 64 * r + 32 * hf, o);
 #pragma unroll
               for (int k = 0; k < 16; ++k)
                 w[16 * hf + k] =
                     pack_bf16x2(__uint_as_float(o[2 * k]) * pend_sc, __uint_as_float(o[2 * k + 1]) * pend_sc);
             }
           } else {
-            tmem_ld32(to + 32 * r, w);
-            tmem_wait_ld();
+            tmem_ld32_wait(to + 32 * r, w);
 #pragma unroll
             for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * pend_sc);
           }
@@ -722,50 +758,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           auto seen = [&](int c) -> bool { return (uint32_t)(c - c0) < (uint32_t)cnt; };
           const bool full = __all_sync(0xffffffffu, cnt == kBlockSize);
           // x = S * 2^-j * f with the key's factor f = s * scale * log2 e; the maximum is of
-          // x + log2 f, the logarithm read off the factor's bits (exponent and mantissa as a
-          // fixed-point number: at most 0.087 below it)
+          // z = x + log2 f.  The table holds f and lg = 2^15 (log2 f + 383), the logarithm read
+          // off f's bits (at most 0.087 low); z is kept in lg's units.
           const float4* tab = reinterpret_cast<const float4*>(smem + kSmemTab + buf * kTabBytes) + 16 * (2 * hk + g);
           uint32_t sr[32];
           // scores of the 32 keys from c on (hidden ones -inf, whose weight 2^-inf is 0)
           auto load_scores = [&](int c) {
-            tmem_ld32(ts + c, sr);
-            tmem_wait_ld();
+            tmem_ld32_wait(ts + c, sr);
             if (!full) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!seen(c + i)) sr[i] = 0xff800000u;
             }
           };
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto score = [&](int i) -> float { return __uint_as_float(sr[i]); };
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+          const uint64_t rsz = pair(rs * kLogUnit, rs * kLogUnit);
 #pragma unroll 1
           for (int c = 0; c < 64; c += 32) {
             load_scores(c);
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 f = tab[(c + i) >> 2];
-              const float k[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                // 2^23 + the factor's upper 23 bits, as a float: log2 in steps of 2^-15, 383 high
-                const float lg = __uint_as_float(__byte_perm(__float_as_uint(k[e]), 0x4B000000u, 0x7321));
-                mx[e] = fmaxf(mx[e], fmaf(lg, 0x1p-15f, __uint_as_float(sr[i + e]) * (k[e] * rs)));
-              }
+              const float4 f = tab[(c + i) >> 2], lg = tab[64 + ((c + i) >> 2)];
+              float z0, z1, z2, z3;
+              unpair(fma2(mul2(pair(score(i), score(i + 1)), pair(f.x, f.y)), rsz, pair(lg.x, lg.y)), z0, z1);
+              unpair(fma2(mul2(pair(score(i + 2), score(i + 3)), pair(f.z, f.w)), rsz, pair(lg.z, lg.w)), z2, z3);
+              mx0 = max3(mx0, z0, z1);
+              mx1 = max3(mx1, z2, z3);
             }
           }
-          ctrl.red_max[buf][2 * hk + g][m] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          ctrl.red_max[buf][2 * hk + g][m] = fmaxf(mx0, mx1);
           go = named_bar_and(kBarSoftmax, kNumSoftmaxThreads, ok);
           if (!go) break;
           const float m_new =
               fmaxf(fmaxf(m_used, fmaxf(ctrl.red_max[buf][0][m], ctrl.red_max[buf][1][m])),
                     fmaxf(ctrl.red_max[buf][2][m], ctrl.red_max[buf][3][m]));
-          const bool rescale = m_new > m_used + kRescaleThreshold;
+          const bool rescale = m_new > m_used + kRescaleThreshold * kLogUnit;
           float alpha = 1.f;
           if (rescale) {
-            alpha = (m_used == -INFINITY) ? 0.f : fast_exp2(m_used - m_new);
+            alpha = (m_used == -INFINITY) ? 0.f : fast_exp2((m_used - m_new) * (1.0f / kLogUnit));
             m_used = m_new;
             l_part *= alpha;
           }
-          const float nref = (m_used == -INFINITY) ? 0.f : kBias - m_used;
+          const float nref = (m_used == -INFINITY) ? 0.f : kBias - m_used * (1.0f / kLogUnit);
+          // weights: P of keys 0..31 in pa, of 32..63 in pb (8 words of hi, 8 of lo terms)
+          uint64_t l01 = pair(0.f, 0.f), l23 = l01;
+          const uint64_t rs2 = pair(rs, rs), nref2 = pair(nref, nref);
+          uint32_t pa[16], pb[16] = {};
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) pa[q] = pb[q];
+            load_scores(c);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 f = tab[(c >> 2) + q];
+              const uint64_t f01 = pair(f.x, f.y), f23 = pair(f.z, f.w);
+              float e0, e1, e2, e3;
+              unpair(fma2(mul2(pair(score(4 * q), score(4 * q + 1)), f01), rs2, nref2), e0, e1);
+              unpair(fma2(mul2(pair(score(4 * q + 2), score(4 * q + 3)), f23), rs2, nref2), e2, e3);
+              const uint64_t e01 = pair(fast_exp2(e0), fast_exp2(e1)), e23 = pair(fast_exp2(e2), fast_exp2(e3));
+              l01 = add2(l01, e01);
+              l23 = add2(l23, e23);
+              unpair(mul2(e01, f01), e0, e1);
+              unpair(mul2(e23, f23), e2, e3);
+              split4(e0, e1, e2, e3, pb[q], pb[8 + q]);
+            }
+          }
+          {
+            float l0, l1;
+            unpair(add2(l01, l23), l0, l1);
+            l_part += l0 + l1;
+          }
           // PV of the previous tile (possibly the previous piece's last) must be done before
           // P is overwritten, O is rescaled or the previous piece's O is read
           if (qk_count >= 1) {
@@ -782,8 +846,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
               for (int c = 0; c < 128; c += 32) {
                 uint32_t o[32];
-                tmem_ld32(to + c, o);
-                tmem_wait_ld();
+                tmem_ld32_wait(to + c, o);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
                 asm volatile(
@@ -804,46 +867,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // 64 keys are granules 4g..4g+3 of its row (granule j at j ^ (m & 7)).  A block with
           // hidden rows has its keys where its V rows were loaded, 64 - hi further on or c0
           // further back: as a rotation, for the hidden keys' zeros belong where these leave.
-          float l0 = 0.f, l1 = 0.f;
           const uint32_t prow = sP + hk * kBoxBytes + m * 128;
           const int turn = hi < kBlockSize ? kBlockSize - hi : kBlockSize - c0;  // 64: none
-#pragma unroll 1
-          for (int c = 0; c < 64; c += 32) {
-            load_scores(c);
+          auto put = [&](const uint32_t (&w)[16], int c) {
+            if (turn == kBlockSize) {  // warp-uniform
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint32_t ph[4], pl[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float4 f = tab[(c >> 2) + 4 * j + q];
-                const uint32_t* x = &sr[16 * j + 4 * q];
-                const float e0 = fast_exp2(fmaf(__uint_as_float(x[0]), f.x * rs, nref));
-                const float e1 = fast_exp2(fmaf(__uint_as_float(x[1]), f.y * rs, nref));
-                const float e2 = fast_exp2(fmaf(__uint_as_float(x[2]), f.z * rs, nref));
-                const float e3 = fast_exp2(fmaf(__uint_as_float(x[3]), f.w * rs, nref));
-                l0 += e0 + e1;
-                l1 += e2 + e3;
-                split4(e0 * f.x, e1 * f.y, e2 * f.z, e3 * f.w, ph[q], pl[q]);
-              }
-              if (turn == kBlockSize) {  // warp-uniform
+              for (int j = 0; j < 2; ++j) {
                 const uint32_t a = prow + (((4 * g + (c >> 4) + j) ^ (m & 7)) << 4);
-                st_shared_v4(a, ph[0], ph[1], ph[2], ph[3]);
-                st_shared_v4(a + 2 * kBoxBytes, pl[0], pl[1], pl[2], pl[3]);
-              } else {
+                st_shared_v4(a, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                st_shared_v4(a + 2 * kBoxBytes, w[8 + 4 * j], w[8 + 4 * j + 1], w[8 + 4 * j + 2], w[8 + 4 * j + 3]);
+              }
+            } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+              for (int q = 0; q < 8; ++q) {
 #pragma unroll 1
-                  for (int e = 0; e < 4; ++e) {
-                    const int k = (c + 16 * j + 4 * q + e + turn) & 63;
-                    const uint32_t a = prow + (((4 * g + (k >> 4)) ^ (m & 7)) << 4) + (k & 15);
-                    st_shared_u8(a, ph[q] >> (8 * e));
-                    st_shared_u8(a + 2 * kBoxBytes, pl[q] >> (8 * e));
-                  }
+                for (int e = 0; e < 4; ++e) {
+                  const int k = (c + 4 * q + e + turn) & 63;
+                  const uint32_t a = prow + (((4 * g + (k >> 4)) ^ (m & 7)) << 4) + (k & 15);
+                  st_shared_u8(a, w[q] >> (8 * e));
+                  st_shared_u8(a + 2 * kBoxBytes, w[8 + q] >> (8 * e));
                 }
               }
             }
-          }
-          l_part += l0 + l1;
+          };
+          put(pa, 0);
+          put(pb, 32);
           fence_proxy_async_smem();
           tc_fence_before();
           named_bar_sync(kBarSoftmax, kNumSoftmaxThreads);
@@ -872,7 +920,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         pend_sc = (bad || l_row != l_row) ? nanf_ : ((l_row > 0.f) ? 1.f / (l_row * p.scale_log2) : 0.f);
         pend_lse = (bad || l_row != l_row)
                        ? nanf_
-                       : ((l_row > 0.f) ? (m_used - kBias + __log2f(l_row)) * 0.69314718055994531f : -INFINITY);
+                       : ((l_row > 0.f) ? (m_used * (1.0f / kLogUnit) - kBias + __log2f(l_row)) * 0.69314718055994531f : -INFINITY);
         pend_direct = (nsplit == 1);
         pend_b = pc.b;
         pend_slot = split_base + pc.split;
@@ -909,155 +957,165 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         else
           mbar_arrive_remote(leader_bar);
       };
-      // ---- query rows: warp pw takes rows 16pw.. of this CTA, four at a time; lane l holds
-      // values 16l.. of q_nope (granule l % 8 of chunk l / 8) and 2l.. of q_pe
-      constexpr int kBatch = 2;
-      uint4 qa[kBatch], qb[kBatch];
-      uint32_t qr[kBatch];
-      auto load_rows = [&](int b, int r0) {
+      // ---- query rows: they land as nine 64-column bf16 boxes and become terms in place.
+      // A warp takes a row at a time (two rows in flight): lane l holds values 16l.. of
+      // q_nope, whose hi and lo terms are granule l % 8 of boxes 2 (l / 8) and 2 (l / 8) + 1,
+      // where values of the same row lay, and 2l.. of q_pe.
+      constexpr int kQBytes = 9 * kBoxBytes;
+      auto load_q = [&](int b) {  // by warp kPrepWarp0
+        const int row = b * p.M + kRowsPerCta * (int)rank;
+        const uint32_t bar = smem_u32(&ctrl.q_raw);
+        expect_tx_if(lane == 0, bar, kQBytes);
+        __syncwarp();
+        tma_load_2d_if(lane < 9, sQ + (lane < 9 ? lane : 0) * kBoxBytes,
+                       lane < 8 ? (const void*)&p.tm_qn : (const void*)&p.tm_qp, bar, lane < 8 ? 64 * lane : 0, row);
+      };
+      auto split_rows = [&](int piece) {
+#pragma unroll 1
+        for (int m0 = 16 * pw; m0 < 16 * pw + 16; m0 += 2) {
+          uint32_t w[2][8], wr[2];
+          float up[2];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int grow = kRowsPerCta * (int)rank + 16 * pw + r0 + i;
-          const int64_t row = (int64_t)b * p.M + grow;
-          qa[i] = qb[i] = make_uint4(0u, 0u, 0u, 0u);
-          qr[i] = 0u;
-          if (grow < p.M) {
-            const uint4* src = reinterpret_cast<const uint4*>(p.q_nope + row * kDLatent) + 2 * lane;
-            qa[i] = __ldg(src);
-            qb[i] = __ldg(src + 1);
-            qr[i] = __ldg(reinterpret_cast<const uint32_t*>(p.q_pe + row * kDRope) + lane);
+          for (int i = 0; i < 2; ++i) {
+            const int m = m0 + i;
+            const uint32_t a = sQ + (lane >> 2) * kBoxBytes + m * 128;
+            ld_shared_v4(a + (((2 * (lane & 3)) ^ (m & 7)) << 4), &w[i][0]);
+            ld_shared_v4(a + (((2 * (lane & 3) + 1) ^ (m & 7)) << 4), &w[i][4]);
+            wr[i] = ld_shared_u32(sQ + 8 * kBoxBytes + m * 128 + (((lane >> 2) ^ (m & 7)) << 4) + 4 * (lane & 3));
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t mx = wr[i] & 0x7fff7fffu;  // magnitudes order as integers
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, w[i][k] & 0x7fff7fffu);
+            mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+            const int E = (int)(mx >> 7);  // biased exponent of the row's largest value
+            const int j = min(134 - E, kMaxUp);
+            up[i] = __int_as_float((j + 127) << 23);
+            if (lane == 0)
+              ctrl.row_scale[piece & 3][m0 + i] =
+                  E == 255 ? __int_as_float(0x7fc00000) : __int_as_float((127 - j) << 23);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int m = m0 + i;
+            const float u = up[i];
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              split4(bf_lo(w[i][2 * k]) * u, bf_hi(w[i][2 * k]) * u, bf_lo(w[i][2 * k + 1]) * u,
+                     bf_hi(w[i][2 * k + 1]) * u, h[k], l[k]);
+            const uint32_t a = sQ + 2 * (lane >> 3) * kBoxBytes + m * 128 + (((lane & 7) ^ (m & 7)) << 4);
+            st_shared_v4(a, h[0], h[1], h[2], h[3]);
+            st_shared_v4(a + kBoxBytes, l[0], l[1], l[2], l[3]);
+            // rotary chunk: the 64 terms twice, against [k'_hi | k'_lo]
+            uint32_t rh, rl;
+            split4(bf_lo(wr[i]) * u, bf_hi(wr[i]) * u, 0.f, 0.f, rh, rl);
+            const uint32_t row = sQ + 2 * kCodeChunks * kBoxBytes + m * 128 + 2 * (lane & 7);
+            const uint32_t g0 = ((lane >> 3) ^ (m & 7)) << 4, g1 = ((4 + (lane >> 3)) ^ (m & 7)) << 4;
+            st_shared_u16(row + g0, rh);
+            st_shared_u16(row + g1, rh);
+            st_shared_u16(row + kBoxBytes + g0, rl);
+            st_shared_u16(row + kBoxBytes + g1, rl);
           }
         }
       };
-      auto store_rows = [&](int r0, int piece) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int m = 16 * pw + r0 + i;
-          const uint32_t w[8] = {qa[i].x, qa[i].y, qa[i].z, qa[i].w, qb[i].x, qb[i].y, qb[i].z, qb[i].w};
-          uint32_t mx = qr[i] & 0x7fff7fffu;  // magnitudes order as integers
-#pragma unroll
-          for (int k = 0; k < 8; ++k) mx = __vmaxu2(mx, w[k] & 0x7fff7fffu);
-          mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-          const int E = (int)(mx >> 7);  // biased exponent of the row's largest value
-          const int j = min(134 - E, kMaxUp);
-          const float up = __int_as_float((j + 127) << 23);
-          if (lane == 0)
-            ctrl.row_scale[piece & 3][m] = E == 255 ? __int_as_float(0x7fc00000) : __int_as_float((127 - j) << 23);
-          uint32_t h[4], l[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            split4(bf_lo(w[2 * k]) * up, bf_hi(w[2 * k]) * up, bf_lo(w[2 * k + 1]) * up, bf_hi(w[2 * k + 1]) * up, h[k],
-                   l[k]);
-          const uint32_t a = sQ + (lane >> 3) * kBoxBytes + m * 128 + (((lane & 7) ^ (m & 7)) << 4);
-          st_shared_v4(a, h[0], h[1], h[2], h[3]);
-          st_shared_v4(a + kChunks * kBoxBytes, l[0], l[1], l[2], l[3]);
-          // rotary chunk: the 64 terms twice, against [k'_hi | k'_lo]
-          uint32_t rh, rl;
-          split_e4m3x2(bf_lo(qr[i]) * up, bf_hi(qr[i]) * up, rh, rl);
-          const uint32_t row = sQ + kCodeChunks * kBoxBytes + m * 128 + 2 * (lane & 7);
-          const uint32_t g0 = ((lane >> 3) ^ (m & 7)) << 4, g1 = ((4 + (lane >> 3)) ^ (m & 7)) << 4;
-          st_shared_u16(row + g0, rh);
-          st_shared_u16(row + g1, rh);
-          st_shared_u16(row + kChunks * kBoxBytes + g0, rl);
-          st_shared_u16(row + kChunks * kBoxBytes + g1, rl);
-        }
-      };
-      // ---- a tile: thread pt holds the scales of the tile's keys pt and 128 + pt; warp pw
-      // takes the rotary parts of this CTA's keys 32pw.., eight lanes a row
-      const uint8_t* own = nullptr;  // the first of this lane's rotary pieces
+      // ---- a tile: thread pt holds the scales of the tile's keys pt and 128 + pt; the rotary
+      // parts of this CTA's keys land as bf16 and become [k'_hi | k'_lo] in place, eight lanes
+      // a row
       float sA = 0.f, sB = 0.f;
+      int idA = 0, idB = 0;                // blocks of those two keys
+      bool seenA = false, seenB = false;   // whether they are visible
       const int r = pt & 63;
-      bool seenA = false, seenB = false;  // whether those two keys are visible
       auto load_tile = [&](const Piece& pc, const int32_t* bt, int t) {
         const int nb = blocks_in_tile(pc, t), v0 = pc.k_lo + t * kBlocksPerTile, kb = pt >> 6;
-        const uint8_t *blkA = nullptr, *blkB = nullptr;
         seenA = seenB = false;
+        sA = sB = 0.f;
         if (kb < nb) {
           const int32_t id = bt[window_block(pc.w, v0 + kb)];
-          blkA = p.rows + (int64_t)(valid_id(p, id) ? id : 0) * (kBlockSize * kRowBytes8);
+          idA = valid_id(p, id) ? id : 0;
           int lo, hi;
           rows_in_block(pc, t, kb, &lo, &hi);
           seenA = r >= lo && r < hi;
+          sA = __ldg(reinterpret_cast<const float*>(p.rows + ((int64_t)idA * kBlockSize + r) * kRowBytes8 + kOffScale8));
         }
         if (kb + 2 < nb) {
           const int32_t id = bt[window_block(pc.w, v0 + kb + 2)];
-          blkB = p.rows + (int64_t)(valid_id(p, id) ? id : 0) * (kBlockSize * kRowBytes8);
+          idB = valid_id(p, id) ? id : 0;
           int lo, hi;
           rows_in_block(pc, t, kb + 2, &lo, &hi);
           seenB = r >= lo && r < hi;
+          sB = __ldg(reinterpret_cast<const float*>(p.rows + ((int64_t)idB * kBlockSize + r) * kRowBytes8 + kOffScale8));
         }
-        sA = blkA ? __ldg(reinterpret_cast<const float*>(blkA + r * kRowBytes8 + kOffScale8)) : 0.f;
-        sB = blkB ? __ldg(reinterpret_cast<const float*>(blkB + r * kRowBytes8 + kOffScale8)) : 0.f;
-        own = leader ? blkA : blkB;
-        if (own) own += (32 * (pw & 1) + (lane >> 3)) * kRowBytes8 + kOffKpe8 + 16 * (lane & 7);
       };
       auto table_entry = [&](float* tab, int key, float s, bool seen) {
         float f = seen ? s * p.scale_log2 : 1.0f;  // a hidden key's scale may be anything
-        if (f < kMinFactor) f = kMinFactor;        // a NaN stays
+        if (f < kMinFactor) f = kMinFactor;        // a NaN stays one
         tab[key] = f;
+        tab[kTileKeys + key] = (float)(__float_as_int(f) >> 8) + 0x1p23f;
       };
-      auto store_rotary = [&]() {
-        // this lane's 8 values of a row: half (lane & 1) of granule (lane % 8) / 2 of the hi
-        // terms, and of granule 4 + (lane % 8) / 2 of the lo terms
+      auto split_rotary = [&]() {
         const int j = lane & 7;
 #pragma unroll 1
         for (int k0 = 0; k0 < 8; k0 += 2) {
-          uint4 raw[2];
+          uint32_t w[2][4];
+          const uint32_t box = sRot + (pw >> 1) * kBoxBytes;
+          const int m0 = 32 * (pw & 1) + 4 * k0 + (lane >> 3);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            raw[k] = own ? __ldg(reinterpret_cast<const uint4*>(own + 4 * (k0 + k) * kRowBytes8))
-                         : make_uint4(0u, 0u, 0u, 0u);
+          for (int k = 0; k < 2; ++k) ld_shared_v4(box + (m0 + 4 * k) * 128 + ((j ^ ((m0 + 4 * k) & 7)) << 4), &w[k][0]);
+          __syncwarp();
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int m = 32 * (pw & 1) + 4 * (k0 + k) + (lane >> 3);
+            const int m = m0 + 4 * k;
             uint32_t h0, l0, h1, l1;
-            split4(bf_lo(raw[k].x), bf_hi(raw[k].x), bf_lo(raw[k].y), bf_hi(raw[k].y), h0, l0);
-            split4(bf_lo(raw[k].z), bf_hi(raw[k].z), bf_lo(raw[k].w), bf_hi(raw[k].w), h1, l1);
-            const uint32_t row = sRot + (pw >> 1) * kBoxBytes + m * 128 + 8 * (j & 1);
+            split4(bf_lo(w[k][0]), bf_hi(w[k][0]), bf_lo(w[k][1]), bf_hi(w[k][1]), h0, l0);
+            split4(bf_lo(w[k][2]), bf_hi(w[k][2]), bf_lo(w[k][3]), bf_hi(w[k][3]), h1, l1);
+            // this lane's 8 values: half of granule j / 2 of the hi terms, 4 + j / 2 of the lo
+            const uint32_t row = box + m * 128 + 8 * (j & 1);
             st_shared_v2(row + (((j >> 1) ^ (m & 7)) << 4), h0, h1);
             st_shared_v2(row + (((4 + (j >> 1)) ^ (m & 7)) << 4), l0, l1);
           }
         }
       };
       Walker walk(p, part);
-      Piece cur{}, nxt{};
-      uint32_t tiles = 0;
+      Piece cur;
+      uint32_t tiles = 0, raws = 0;
       int npieces = 0;
-      bool have = walk.next(cur);
-      while (go && have) {
-        const bool have_nxt = walk.next(nxt);
+      while (go && walk.next(cur)) {
         const int32_t* bt = unit_table(p, cur.b);
-        load_rows(cur.b, 0);
-        if (have_nxt) {  // the next piece's rows towards L2: 8 lines a row of q_nope, one of q_pe
-          for (int i = pt; i < 9 * kRowsPerCta; i += kNumPrepThreads) {
-            const int grow = kRowsPerCta * (int)rank + i / 9;
-            const int64_t row = (int64_t)nxt.b * p.M + grow;
-            const void* a = i % 9 < 8 ? (const void*)(p.q_nope + row * kDLatent + 64 * (i % 9))
-                                      : (const void*)(p.q_pe + row * kDRope);
-            if (grow < p.M) asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
-          }
-        }
         if (npieces > 0) ok = wait_bar(&ctrl, p, smem_u32(&ctrl.q_empty), (npieces - 1) & 1) && ok;
-        if (ok) {
-#pragma unroll 1
-          for (int r0 = 0; r0 < 16; r0 += kBatch) {
-            if (r0 > 0) load_rows(cur.b, r0);
-            store_rows(r0, npieces);
-          }
-        }
+        // a wait that ran out in another warp shows at the next publish; this one loads only
+        // after its own wait, so the buffer is free
+        if (pw == 0 && __all_sync(0xffffffffu, ok)) load_q(cur.b);
+        load_tile(cur, bt, 0);
+        ok = wait_bar(&ctrl, p, smem_u32(&ctrl.q_raw), npieces & 1) && ok;
+        if (ok) split_rows(npieces);
         if (!publish()) break;
         if (pt == 0) arrive(&ctrl.q_full, q_full_l);
         const int nt = num_tiles(cur);
-        load_tile(cur, bt, 0);
         for (int t = 0; t < nt && go; ++t) {
           const uint32_t buf = tiles & 1;
-          if (tiles >= 2) ok = wait_bar(&ctrl, p, smem_u32(&ctrl.sc_empty[buf]), ((tiles >> 1) - 1) & 1) && ok;
+          const int own = min(max(blocks_in_tile(cur, t) - 2 * (int)rank, 0), 2);
           if (tiles >= 1) ok = wait_bar(&ctrl, p, smem_u32(&ctrl.k_empty), (tiles - 1) & 1) && ok;
+          if (own > 0) {
+            // lane 0 of the two even warps brings the block whose scales it holds
+            const uint32_t bar = smem_u32(&ctrl.k_raw);
+            const bool all = __all_sync(0xffffffffu, ok);
+            expect_tx_if(all && pt == 0, bar, own * kBoxBytes);
+            tma_load_3d_if(all && lane == 0 && !(pw & 1) && (pw >> 1) < own, sRot + (pw >> 1) * kBoxBytes, &p.tm_rows,
+                           bar, kOffKpe8, 0, leader ? idA : idB);
+          }
+          if (tiles >= 2) ok = wait_bar(&ctrl, p, smem_u32(&ctrl.sc_empty[buf]), ((tiles >> 1) - 1) & 1) && ok;
           if (ok) {
             float* tab = tables + buf * (kTabBytes / 4);
             table_entry(tab, pt, sA, seenA);
             table_entry(tab, 128 + pt, sB, seenB);
-            store_rotary();
+          }
+          if (t + 1 < nt) load_tile(cur, bt, t + 1);
+          if (own > 0) {
+            ok = wait_bar(&ctrl, p, smem_u32(&ctrl.k_raw), raws & 1) && ok;
+            ++raws;
+            if ((pw >> 1) < own && __all_sync(0xffffffffu, ok)) split_rotary();
           }
           if (!publish()) break;
           if (pt == 0) {
@@ -1065,11 +1123,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             arrive(&ctrl.k_full, k_full_l);
           }
           ++tiles;
-          if (t + 1 < nt) load_tile(cur, bt, t + 1);
         }
         ++npieces;
-        cur = nxt;
-        have = have_nxt;
       }
     }
     // the peer CTA's MMA warp has no role; it joins its warpgroup's register release
@@ -1122,9 +1177,9 @@ cudaError_t window_fp8_setup() {
   return cudaFuncSetAttribute(window_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemDyn + 1024);
 }
 
-cudaError_t launch_window_fp8(const CUtensorMap& tm_rows, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
-                              const void* rows, const void* q_nope, const void* q_pe, const int32_t* block_table,
-                              int max_blocks, const int32_t* seqlens, const int32_t* q_lens, const int32_t* meta,
+cudaError_t launch_window_fp8(const CUtensorMap& tm_rows, const CUtensorMap& tm_qn, const CUtensorMap& tm_qp,
+                              const CUtensorMap& tm_out, const CUtensorMap& tm_part, const void* rows,
+                              const int32_t* block_table, int max_blocks, const int32_t* seqlens, const int32_t* q_lens, const int32_t* meta,
                               int64_t num_blocks, int units, int rep, int H, float scale, int window, int sinks,
                               void* out, float* lse, float* part_lse, int32_t* status, int num_ctas,
                               uint64_t wait_timeout_ns, int inject_stall, cudaStream_t stream) {
@@ -1134,8 +1189,8 @@ cudaError_t launch_window_fp8(const CUtensorMap& tm_rows, const CUtensorMap& tm_
   prm.tm_out = tm_out;
   prm.tm_part = tm_part;
   prm.rows = static_cast<const uint8_t*>(rows);
-  prm.q_nope = static_cast<const __nv_bfloat16*>(q_nope);
-  prm.q_pe = static_cast<const __nv_bfloat16*>(q_pe);
+  prm.tm_qn = tm_qn;
+  prm.tm_qp = tm_qp;
   prm.block_table = block_table;
   prm.seqlens = seqlens;
   prm.q_lens = q_lens;
