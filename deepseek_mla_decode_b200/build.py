@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libmla.so")
 SOURCES = ["mla_api.cu", "mla_metadata.cu", "mla_decode_kernel.cu", "mla_combine.cu", "mla_noalloc.cu",
            "mla_absorb.cu", "mla_fp8.cu", "mla_rope.cu", "mla_append.cu", "mla_window_fp8.cu",
            "sage_quant.cu", "sage_attn.cu"]
-HEADERS = ["mla_internal.h", "mla_rope.cuh", "pair_ptx.cuh", "ptx_sm100.cuh", "sage_internal.h"]
+HEADERS = ["mla_internal.h", "mla_rope.cuh", "mla_window.cuh", "pair_ptx.cuh", "ptx_sm100.cuh", "sage_internal.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

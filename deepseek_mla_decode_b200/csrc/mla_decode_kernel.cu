@@ -49,6 +49,7 @@
 #include <cstdint>
 #include <cstring>
 #include "mla_internal.h"
+#include "mla_window.cuh"
 #include "pair_ptx.cuh"
 #include "ptx_sm100.cuh"
 
@@ -339,12 +340,11 @@ __device__ __forceinline__ int clamp_block_id(const Params& p, int32_t id) {
 // current length (NaN and MLA_DEVICE_ERR_METADATA).  Partition `part` takes the
 // sequences b with b % P == part; the 32 lanes of one warp write this CTA's 64 rows
 // [y0, y0 + 64) of the row tile that starts at row0.
-template <bool kWin>
 __device__ __forceinline__ void write_orphan_rows(const Params& p, int part, int P, int row0, int y0, int lane) {
   const int32_t* nblk = p.meta + off_nblk();
   for (int b = part; b < p.B; b += P) {
     const int n = seq_len(p, b);
-    const int want = expected_blocks<kWin>(p, n);
+    const int want = expected_blocks<false>(p, n);
     const int ql = query_len(p, b);
     const bool bad_len = want < 0 || ql < 0;
     const bool stale = !bad_len && nblk[b] != want;
@@ -675,8 +675,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       }
       if (ok && prv_t >= 0) issue_pv(prv, prv_base, prv_t);
       // With its loads issued, producer warp 0 writes the rows that no partition
-      // covers while the last tiles are still being computed.
-      if (pi == 0) write_orphan_rows<kWin>(p, part, P, tile_row0, tile_row0 + kRowsPerCta * (int)rank, lane);
+      // covers while the last tiles are still being computed (kWin: an idle warp does).
+      if (!kWin && pi == 0) write_orphan_rows(p, part, P, tile_row0, tile_row0 + kRowsPerCta * (int)rank, lane);
     }
     // =======================================================================
     // MMA issuer (leader CTA only)
@@ -1344,9 +1344,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         if (go && prv_t >= 0) conv_pv(prv, prv_t);
       }
     }
-    // the peer CTA's MMA warp has no role; it joins its warpgroup's register release
+    // the peer CTA's MMA warp has no role; it joins its warpgroup's register release, and
+    // with a window writes the rows of units that no piece covers
     else if (warp == kMmaWarp) {
       if constexpr (kFp8) regs_dec<kRegsIssue>();
+      if constexpr (kWin)
+        write_orphan_units(p.meta, p.B, p.M, p.window, p.sinks, part, P, lane, [&](int u) { return seq_len(p, u); },
+                           p.out, p.lse, p.status);
     }
   }
 

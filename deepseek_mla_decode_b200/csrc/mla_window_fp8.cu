@@ -34,6 +34,7 @@
 #include <cstdint>
 #include <cstring>
 #include "mla_internal.h"
+#include "mla_window.cuh"
 #include "pair_ptx.cuh"
 #include "ptx_sm100.cuh"
 
@@ -157,8 +158,8 @@ __device__ __forceinline__ const int32_t* unit_table(const Params& p, int u) {
 }
 
 // Walks the pieces of one partition; units with an invalid length, or a block count in the
-// metadata that is not the one their length needs, are skipped by every role alike (warp 0
-// writes their NaN rows).
+// metadata that is not the one their length needs, are skipped by every role alike (an idle
+// warp writes their NaN rows).
 struct Walker {
   const Params* p;
   int cb, ck, be, ke;
@@ -307,31 +308,6 @@ __device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
-// Rows that no piece covers: no visible key (0 / -inf), an invalid length or count (NaN and
-// MLA_DEVICE_ERR_SEQLEN), a stale block count (NaN and MLA_DEVICE_ERR_METADATA).  Partition
-// `part` takes the units b with b % P == part; a warp writes this CTA's rows from y0 on.
-__device__ __forceinline__ void write_orphan_rows(const Params& p, int part, int P, int y0, int lane) {
-  const int32_t* nblk = p.meta + off_nblk();
-  for (int b = part; b < p.B; b += P) {
-    const int n = unit_len(p, b);
-    const bool bad_len = n < 0;
-    const bool stale = !bad_len && nblk[b] != unit_blocks(p, n);
-    if (!bad_len && !stale && n > 0) continue;
-    const bool bad = bad_len || stale;
-    const float v = bad ? __int_as_float(0x7fc00000) : 0.0f;
-    const uint32_t pv = pack_bf16x2(v, v);
-    for (int i = lane; i < kRowsPerCta * (kDLatent / 8); i += 32) {  // 16-byte units
-      const int row = y0 + i / (kDLatent / 8);
-      if (row < p.M)
-        reinterpret_cast<uint4*>(p.out + ((int64_t)b * p.M + row) * kDLatent)[i % (kDLatent / 8)] =
-            make_uint4(pv, pv, pv, pv);
-    }
-    for (int r = lane; r < kRowsPerCta; r += 32)
-      if (y0 + r < p.M) p.lse[(int64_t)b * p.M + y0 + r] = bad ? __int_as_float(0x7fc00000) : -INFINITY;
-    if (bad && lane == 0) set_status(p, bad_len ? kErrSeqlen : kErrMetadata);
-  }
-}
-
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     window_fp8_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -516,7 +492,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (ok && prv_t >= 0) issue_pv(prv, prv_base, prv_t);
-      if (pi == 0) write_orphan_rows(p, part, P, kRowsPerCta * (int)rank, lane);
     }
     // =======================================================================
     // MMA issuer (leader CTA only)
@@ -1127,9 +1102,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++npieces;
       }
     }
-    // the peer CTA's MMA warp has no role; it joins its warpgroup's register release
+    // the peer CTA's MMA warp has no role; it joins its warpgroup's register release and
+    // writes the rows of units that no piece covers
     else if (warp == kMmaWarp) {
       regs_dec<kRegsIssue>();
+      write_orphan_units(p.meta, p.B, p.M, p.window, p.sinks, part, P, lane, [&](int u) { return unit_len(p, u); },
+                         p.out, p.lse, p.status);
     }
   }
 
