@@ -13,11 +13,15 @@
 #include <cuda_bf16.h>
 #include <cmath>
 #include "mla_rope.cuh"
+#include "ptx_sm100.cuh"
 
 namespace mla {
+
+using namespace ptx;
+
 namespace {
 
-constexpr int kWarpsPerBlock = 8;
+constexpr int kWarpsPerBlock = 4;
 
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -46,9 +50,31 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t codes4(const float* f, float scale) {
+// Codes of 16 values over scale, as IEEE quotients rounded to e4m3.  Products by 1/scale
+// shrunk and stretched by 2^-21 (1/scale and the product are each off by 2^-24) bracket the
+// quotient, and rounding keeps order: where both give the same codes, those are the
+// quotient's.  That holds for all but about one value in 2^16; the others are divided.
+__device__ __forceinline__ uint32_t codes4(const float* f, float r) {
+  return e4m3x2(f[0] * r, f[1] * r) | (e4m3x2(f[2] * r, f[3] * r) << 16);
+}
+__device__ __forceinline__ uint32_t divided_codes4(const float* f, float scale) {
   return e4m3x2(__fdiv_rn(f[0], scale), __fdiv_rn(f[1], scale)) |
          (e4m3x2(__fdiv_rn(f[2], scale), __fdiv_rn(f[3], scale)) << 16);
+}
+__device__ __forceinline__ void codes16(const float (&c0)[8], const float (&c1)[8], float scale, uint32_t (&q)[4]) {
+  const float r = __frcp_rn(scale);
+  const float below = r * (1.0f - 0x1p-21f), above = r * (1.0f + 0x1p-21f);
+  bool same = scale > 0x1p-100f && scale < 0x1p100f;  // 1/scale is a normal number
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float* f = (i < 2 ? c0 : c1) + 4 * (i & 1);
+    q[i] = codes4(f, below);
+    same = same && q[i] == codes4(f, above);
+  }
+  if (!same) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = divided_codes4((i < 2 ? c0 : c1) + 4 * (i & 1), scale);
+  }
 }
 
 struct AppendParams {
@@ -59,11 +85,13 @@ struct AppendParams {
   const int32_t* q_lens;
   int32_t* status;
   uint8_t* cache;
-  int64_t row_stride, rows, num_blocks;
-  int max_blocks, s_q;
+  int64_t row_stride, num_blocks;
+  uint32_t rows;
+  int max_blocks;
   float eps;
   int rotate;  // 0: store k as given
   int half_layout;
+  RowDiv per_seq;  // tokens a sequence
   RopeTurns rope;
 };
 
@@ -72,44 +100,48 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32) append_kernel(const __gri
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
+  const uint32_t row = blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
   if (row >= p.rows) return;
-  const int b = (int)(row / p.s_q), i = (int)(row - (int64_t)b * p.s_q);
   // the row's loads do not wait for the sequence's words
-  const __nv_bfloat16* src = p.x + row * p.row_stride;
+  const int i0 = p.half_layout ? lane : 2 * lane, i1 = p.half_layout ? lane + 32 : 2 * lane + 1;
+  const __nv_bfloat16* src = p.x + (int64_t)row * p.row_stride;
   const uint4 v0 = reinterpret_cast<const uint4*>(src)[lane];
   const uint4 v1 = reinterpret_cast<const uint4*>(src)[lane + 32];
-  const int i0 = p.half_layout ? lane : 2 * lane, i1 = p.half_layout ? lane + 32 : 2 * lane + 1;
   float a = __bfloat162float(src[kDLatent + i0]), d = __bfloat162float(src[kDLatent + i1]);
+  const int s_q = (int)p.per_seq.d, b = p.per_seq.quotient(row), i = (int)(row - (uint32_t)b * p.per_seq.d);
   const int n = p.seqlens[b];
-  int pos = token_position(n, p.q_lens ? p.q_lens[b] : p.s_q, i, p.s_q);
+  int pos = token_position(n, p.q_lens ? p.q_lens[b] : s_q, i, s_q);
   if ((int64_t)n > (int64_t)p.max_blocks * kBlockSize) pos = kTokenBad;
-  if (pos < 0) {
-    if (pos == kTokenBad && lane == 0 && p.status) atomicOr(p.status, kErrSeqlen);
-    return;
-  }
-  const int32_t block = p.block_table[(int64_t)b * p.max_blocks + pos / kBlockSize];
-  if (block < 0 || (int64_t)block >= p.num_blocks) {
-    if (lane == 0 && p.status) atomicOr(p.status, kErrBlockId);
+  const int32_t block = pos >= 0 ? p.block_table[(int64_t)b * p.max_blocks + pos / kBlockSize] : -1;
+  if (pos < 0 || block < 0 || (int64_t)block >= p.num_blocks) {
+    if (lane == 0 && p.status && pos != kTokenNone) atomicOr(p.status, pos < 0 ? kErrSeqlen : kErrBlockId);
     return;
   }
   float c0[8], c1[8];
   unpack8(v0, c0);
   unpack8(v1, c1);
-  if (p.weight) {
+  if (p.weight) {  // in packed pairs: the kernel issues instructions two thirds of the time
     float w0[8], w1[8];
     unpack8(reinterpret_cast<const uint4*>(p.weight)[lane], w0);
     unpack8(reinterpret_cast<const uint4*>(p.weight)[lane + 32], w1);
-    float ss = 0.f;
+    uint64_t s0 = pack_f32x2(0.f, 0.f), s1 = s0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss += c0[e] * c0[e] + c1[e] * c1[e];
+    for (int e = 0; e < 8; e += 2) {
+      const uint64_t x0 = pack_f32x2(c0[e], c0[e + 1]), x1 = pack_f32x2(c1[e], c1[e + 1]);
+      s0 = fma2(x0, x0, s0);
+      s1 = fma2(x1, x1, s1);
+    }
+    float ss, odd;
+    unpack_f32x2(add2(s0, s1), ss, odd);
+    ss += odd;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float r = rsqrtf(ss * (1.0f / kDLatent) + p.eps);
+    const uint64_t rr = pack_f32x2(r, r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      c0[e] = c0[e] * r * w0[e];
-      c1[e] = c1[e] * r * w1[e];
+    for (int e = 0; e < 8; e += 2) {
+      unpack_f32x2(mul2(mul2(pack_f32x2(c0[e], c0[e + 1]), rr), pack_f32x2(w0[e], w0[e + 1])), c0[e], c0[e + 1]);
+      unpack_f32x2(mul2(mul2(pack_f32x2(c1[e], c1[e + 1]), rr), pack_f32x2(w1[e], w1[e + 1])), c1[e], c1[e + 1]);
     }
   }
   if (p.rotate) {
@@ -127,17 +159,16 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32) append_kernel(const __gri
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float scale = __fdiv_rn(amax, 448.0f);
-    uint2 q0 = make_uint2(0u, 0u), q1 = q0;
+    uint32_t q[4] = {0u, 0u, 0u, 0u};
     float ka = 0.f, kd = 0.f;
     if (scale > 0.f) {
-      q0 = make_uint2(codes4(c0, scale), codes4(c0 + 4, scale));
-      q1 = make_uint2(codes4(c1, scale), codes4(c1 + 4, scale));
+      codes16(c0, c1, scale, q);
       ka = __fdiv_rn(a, scale);
       kd = __fdiv_rn(d, scale);
     }
     uint8_t* dst = p.cache + slot * kRowBytes8;
-    reinterpret_cast<uint2*>(dst)[lane] = q0;
-    reinterpret_cast<uint2*>(dst)[lane + 32] = q1;
+    reinterpret_cast<uint2*>(dst)[lane] = make_uint2(q[0], q[1]);
+    reinterpret_cast<uint2*>(dst)[lane + 32] = make_uint2(q[2], q[3]);
     __nv_bfloat16* kp = reinterpret_cast<__nv_bfloat16*>(dst + kOffKpe8);
     kp[i0] = __float2bfloat16_rn(ka);
     kp[i1] = __float2bfloat16_rn(kd);
@@ -165,7 +196,7 @@ mla_status_t append_any(bool fp8, const void* kv_a, int64_t row_stride, const vo
   const uintptr_t words = reinterpret_cast<uintptr_t>(cache_seqlens) | reinterpret_cast<uintptr_t>(q_lens) |
                           reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(status);
   if ((wide & 15u) || (words & 3u)) return MLA_ERR_INVALID_ARG;
-  AppendParams p = {};
+  AppendParams p = {.per_seq = RowDiv(s_q)};
   if (rope && !rope_turns(rope, &p.rope)) return MLA_ERR_INVALID_ARG;
   int sms = 0;
   mla_status_t st = mla_device_sm_count(&sms);
@@ -178,15 +209,14 @@ mla_status_t append_any(bool fp8, const void* kv_a, int64_t row_stride, const vo
   p.status = status;
   p.cache = static_cast<uint8_t*>(cache);
   p.row_stride = row_stride;
-  p.rows = (int64_t)B * s_q;
+  p.rows = (uint32_t)B * (uint32_t)s_q;
   p.num_blocks = num_blocks;
   p.max_blocks = max_blocks;
-  p.s_q = s_q;
   p.eps = eps;
   p.rotate = rope != nullptr;
   p.half_layout = rope ? rope->half_layout : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.rows + kWarpsPerBlock - 1) / kWarpsPerBlock));
+  cfg.gridDim = dim3((p.rows + kWarpsPerBlock - 1) / kWarpsPerBlock);
   cfg.blockDim = dim3(kWarpsPerBlock * 32);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];

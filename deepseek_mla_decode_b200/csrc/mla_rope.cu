@@ -31,17 +31,18 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 // rotary part is rotated in place.  kHalf: pair i = (x[i], x[i + 32]), else (x[2i], x[2i+1]).
 template <bool kHalf, bool kSplit>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32) rope_q_kernel(
-    const __nv_bfloat16* q, int64_t row_stride, const int32_t* seqlens, const int32_t* q_lens, int64_t rows, int s_q,
-    int H, int groups, const __grid_constant__ RopeTurns rope, __nv_bfloat16* q_heads, __nv_bfloat16* q_pe,
+    const __nv_bfloat16* q, int64_t row_stride, const int32_t* seqlens, const int32_t* q_lens, uint32_t rows,
+    const __grid_constant__ RowDiv per_seq, int H, const __grid_constant__ RopeTurns rope, __nv_bfloat16* q_heads, __nv_bfloat16* q_pe,
     int32_t* status) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
-  const int64_t row = unit / groups;
-  if (row >= rows) return;
-  const int h0 = (int)(unit - row * groups) * kHeadsPerWarp;
-  const int b = (int)(row / s_q), i = (int)(row - (int64_t)b * s_q);
+  // block (x, y): rows of a group of kHeadsPerWarp heads
+  const uint32_t row32 = blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5);
+  if (row32 >= rows) return;
+  const int64_t row = row32;
+  const int h0 = (int)blockIdx.y * kHeadsPerWarp, s_q = (int)per_seq.d;
+  const int b = per_seq.quotient(row32), i = (int)(row32 - (uint32_t)b * per_seq.d);
   const int pos = token_position(seqlens[b], q_lens ? q_lens[b] : s_q, i, s_q);
   if (pos == kTokenBad && h0 == 0 && lane == 0 && status) atomicOr(status, kErrSeqlen);
   float c = 0.f, s = 0.f;
@@ -120,11 +121,9 @@ mla_status_t rope_q_any(const void* q, int64_t row_stride, const int32_t* cache_
   mla_status_t st = mla_device_sm_count(&sms);
   if (st != MLA_OK) return st;
   const int64_t rows = (int64_t)B * s_q;
-  const int groups = (H + kHeadsPerWarp - 1) / kHeadsPerWarp;
-  const int64_t blocks = (rows * groups + kWarpsPerBlock - 1) / kWarpsPerBlock;
-  if (blocks > 0x7fffffffLL) return MLA_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)((rows + kWarpsPerBlock - 1) / kWarpsPerBlock),
+                     (unsigned)((H + kHeadsPerWarp - 1) / kHeadsPerWarp));
   cfg.blockDim = dim3(kWarpsPerBlock * 32);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -135,8 +134,8 @@ mla_status_t rope_q_any(const void* q, int64_t row_stride, const int32_t* cache_
   const bool split = q_heads != nullptr;
   auto* kernel = rope->half_layout ? (split ? rope_q_kernel<true, true> : rope_q_kernel<true, false>)
                                    : (split ? rope_q_kernel<false, true> : rope_q_kernel<false, false>);
-  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<const __nv_bfloat16*>(q), row_stride, cache_seqlens, q_lens, rows,
-                         s_q, H, groups, turns, static_cast<__nv_bfloat16*>(q_heads),
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<const __nv_bfloat16*>(q), row_stride, cache_seqlens, q_lens,
+                         (uint32_t)rows, RowDiv(s_q), H, turns, static_cast<__nv_bfloat16*>(q_heads),
                          static_cast<__nv_bfloat16*>(q_pe), status) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
@@ -145,13 +144,16 @@ mla_status_t rope_q_any(const void* q, int64_t row_stride, const int32_t* cache_
 }  // namespace
 
 bool rope_turns(const mla_rope_t* rope, RopeTurns* out) {
-  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  constexpr long double kTwoPi = 6.283185307179586476925286766559L;
   if (rope->half_layout != 0 && rope->half_layout != 1) return false;
   if (!std::isfinite(rope->amplitude)) return false;
   for (int i = 0; i < kDRope / 2; ++i) {
-    // beyond this a position of 2^31 has no fraction of a turn left in 64 bits
+    // beyond this extended precision keeps too little of a turn's fraction
     if (!(std::fabs(rope->freq[i]) <= 1e6)) return false;
-    out->turns[i] = rope->freq[i] / kTwoPi;
+    long double t = rope->freq[i] / kTwoPi;
+    t -= std::floor(t);
+    t *= 18446744073709551616.0L;
+    out->turns[i] = t >= 18446744073709551615.0L ? 0u : static_cast<uint64_t>(t);
   }
   out->amplitude = rope->amplitude;
   return true;

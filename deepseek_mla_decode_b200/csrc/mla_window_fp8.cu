@@ -259,28 +259,6 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
   hi = e4m3x4(ta, tb, tc, td);
   lo = e4m3x4(a - ta, b - tb, c - tc, d - td);
 }
-// packed pairs of fp32
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -748,7 +726,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           };
           auto score = [&](int i) -> float { return __uint_as_float(sr[i]); };
           float mx0 = -INFINITY, mx1 = -INFINITY;
-          const uint64_t rsz = pair(rs * kLogUnit, rs * kLogUnit);
+          const uint64_t rsz = pack_f32x2(rs * kLogUnit, rs * kLogUnit);
 #pragma unroll 1
           for (int c = 0; c < 64; c += 32) {
             load_scores(c);
@@ -756,8 +734,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; i += 4) {
               const float4 f = tab[(c + i) >> 2], lg = tab[64 + ((c + i) >> 2)];
               float z0, z1, z2, z3;
-              unpair(fma2(mul2(pair(score(i), score(i + 1)), pair(f.x, f.y)), rsz, pair(lg.x, lg.y)), z0, z1);
-              unpair(fma2(mul2(pair(score(i + 2), score(i + 3)), pair(f.z, f.w)), rsz, pair(lg.z, lg.w)), z2, z3);
+              unpack_f32x2(fma2(mul2(pack_f32x2(score(i), score(i + 1)), pack_f32x2(f.x, f.y)), rsz, pack_f32x2(lg.x, lg.y)), z0, z1);
+              unpack_f32x2(fma2(mul2(pack_f32x2(score(i + 2), score(i + 3)), pack_f32x2(f.z, f.w)), rsz, pack_f32x2(lg.z, lg.w)), z2, z3);
               mx0 = max3(mx0, z0, z1);
               mx1 = max3(mx1, z2, z3);
             }
@@ -777,8 +755,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           const float nref = (m_used == -INFINITY) ? 0.f : kBias - m_used * (1.0f / kLogUnit);
           // weights: P of keys 0..31 in pa, of 32..63 in pb (8 words of hi, 8 of lo terms)
-          uint64_t l01 = pair(0.f, 0.f), l23 = l01;
-          const uint64_t rs2 = pair(rs, rs), nref2 = pair(nref, nref);
+          uint64_t l01 = pack_f32x2(0.f, 0.f), l23 = l01;
+          const uint64_t rs2 = pack_f32x2(rs, rs), nref2 = pack_f32x2(nref, nref);
           uint32_t pa[16], pb[16] = {};
 #pragma unroll 1
           for (int c = 0; c < 64; c += 32) {
@@ -788,21 +766,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
               const float4 f = tab[(c >> 2) + q];
-              const uint64_t f01 = pair(f.x, f.y), f23 = pair(f.z, f.w);
+              const uint64_t f01 = pack_f32x2(f.x, f.y), f23 = pack_f32x2(f.z, f.w);
               float e0, e1, e2, e3;
-              unpair(fma2(mul2(pair(score(4 * q), score(4 * q + 1)), f01), rs2, nref2), e0, e1);
-              unpair(fma2(mul2(pair(score(4 * q + 2), score(4 * q + 3)), f23), rs2, nref2), e2, e3);
-              const uint64_t e01 = pair(fast_exp2(e0), fast_exp2(e1)), e23 = pair(fast_exp2(e2), fast_exp2(e3));
+              unpack_f32x2(fma2(mul2(pack_f32x2(score(4 * q), score(4 * q + 1)), f01), rs2, nref2), e0, e1);
+              unpack_f32x2(fma2(mul2(pack_f32x2(score(4 * q + 2), score(4 * q + 3)), f23), rs2, nref2), e2, e3);
+              const uint64_t e01 = pack_f32x2(fast_exp2(e0), fast_exp2(e1)), e23 = pack_f32x2(fast_exp2(e2), fast_exp2(e3));
               l01 = add2(l01, e01);
               l23 = add2(l23, e23);
-              unpair(mul2(e01, f01), e0, e1);
-              unpair(mul2(e23, f23), e2, e3);
+              unpack_f32x2(mul2(e01, f01), e0, e1);
+              unpack_f32x2(mul2(e23, f23), e2, e3);
               split4(e0, e1, e2, e3, pb[q], pb[8 + q]);
             }
           }
           {
             float l0, l1;
-            unpair(add2(l01, l23), l0, l1);
+            unpack_f32x2(add2(l01, l23), l0, l1);
             l_part += l0 + l1;
           }
           // PV of the previous tile (possibly the previous piece's last) must be done before

@@ -2,9 +2,9 @@
 
 Tolerances.  A result is rounded once, to half a step: bf16 2^-8, e4m3 2^-4 of its value
 (below the e4m3 normal range half of 2^-9 in units of the scale).  Before that:
-* rotation: the angle is off by at most pi 2^-25 (the reduced fraction in fp32) and cos / sin
-  by 2 ulp, so each product is off by less than 2^-22 of its operand and the sum of two by
-  2^-20 (|a| + |b|) amplitude, with room for the fp32 multiplies;
+* rotation: the angle is off by at most pi 2^-24 = 2^-22.3 (the reduced fraction in fp32) and
+  the fast cos / sin by 2^-21.2, together 2^-20.6 of each operand; with the fp32 multiplies
+  and adds the sum of two products is off by less than 2^-20 (|a| + |b|) amplitude;
 * norm: 512 squares in a tree 16 + 5 deep, rsqrt (2 ulp) and two multiplies: under 2^-19 of
   the value."""
 
