@@ -509,6 +509,16 @@ def _device_index(t):
     return index
 
 
+def _new(like, stream, shape, dtype):
+    """An uninitialised tensor for a launch on `stream`.  It comes from that stream's memory
+    pool: memory of the current stream's pool may still be in use there, and a workspace goes
+    back to its pool before the kernels that use it have run."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _launch_stream(index, stream):
     """The raw handle of `stream`, or of the device's current stream when it is None."""
     if stream is None:
@@ -565,18 +575,19 @@ def rope_q(q, cache_seqlens, rope: Rope, q_lens=None, q_heads=None, q_pe=None, s
     B, s_q, H, _ = q.shape
     row = _token_rows("q", q, (192, 1), H * 192)
     index = _device_index(q)
+    handle = _launch_stream(index, stream)
     _tokens(index, B, cache_seqlens, q_lens, status)
     if q_heads is None:
-        q_heads = q.new_empty((B, s_q, H, 128))
+        q_heads = _new(q, stream, (B, s_q, H, 128), bf16)
     else:
         _expect("q_heads", q_heads, index, bf16, (B, s_q, H, 128))
     if q_pe is None:
-        q_pe = q.new_empty((B, s_q, H, 64))
+        q_pe = _new(q, stream, (B, s_q, H, 64), bf16)
     else:
         _expect("q_pe", q_pe, index, bf16, (B, s_q, H, 64))
     code = (_lib or load_library()).mla_rope_q(
         q.data_ptr(), row, cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, rope, q_heads.data_ptr(),
-        q_pe.data_ptr(), _ptr(status), _launch_stream(index, stream))
+        q_pe.data_ptr(), _ptr(status), handle)
     if code:
         raise MLAError("mla_rope_q", code)
     return q_heads, q_pe
@@ -591,10 +602,10 @@ def rope_inplace(q, cache_seqlens, rope: Rope, q_lens=None, status=None, stream=
     B, s_q, H, _ = q.shape
     row = _token_rows("q", q, (192, 1), H * 192)
     index = _device_index(q)
+    handle = _launch_stream(index, stream)
     _tokens(index, B, cache_seqlens, q_lens, status)
     _check("mla_rope_inplace", (_lib or load_library()).mla_rope_inplace(
-        q.data_ptr(), row, cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, rope, _ptr(status),
-        _launch_stream(index, stream)))
+        q.data_ptr(), row, cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, rope, _ptr(status), handle))
     return q
 
 
@@ -646,14 +657,15 @@ def get_metadata_window(cache_seqlens, q_lens, s_q: int, H: int, window: int, si
     torch = _torch or _torch_module()
     (B,) = cache_seqlens.shape
     index = _device_index(cache_seqlens)
+    handle = _launch_stream(index, stream)
     _tokens(index, B, cache_seqlens, q_lens, None)
     if metadata is None:
-        metadata = cache_seqlens.new_empty(_window_sizes(index, B * s_q, H)[0] // 4)
+        metadata = _new(cache_seqlens, stream, _window_sizes(index, B * s_q, H)[0] // 4, torch.int32)
     else:
         _expect("metadata", metadata, index, torch.int32, None)
     _check("mla_get_metadata_window", (_lib or load_library()).mla_get_metadata_window(
         cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, window, sinks, metadata.data_ptr(), 4 * metadata.numel(),
-        _launch_stream(index, stream)))
+        handle))
     return metadata
 
 
@@ -665,6 +677,7 @@ def _decode_window(fn, q_nope, q_pe, kv, width, dtype, block_table, cache_seqlen
     B, s_q, H, _ = q_nope.shape
     bf16, i32 = torch.bfloat16, torch.int32
     index = _device_index(q_nope)
+    handle = _launch_stream(index, stream)
     max_blocks, num_blocks = block_table.shape[1], kv.shape[0]
     _expect("q_nope", q_nope, index, bf16, (B, s_q, H, 512))
     _expect("q_pe", q_pe, index, bf16, (B, s_q, H, 64))
@@ -673,22 +686,22 @@ def _decode_window(fn, q_nope, q_pe, kv, width, dtype, block_table, cache_seqlen
     _expect("metadata", metadata, index, i32, None)
     _tokens(index, B, cache_seqlens, q_lens, status)
     if workspace is None:
-        workspace = kv.new_empty(_window_sizes(index, B * s_q, H)[1], dtype=torch.uint8)
+        workspace = _new(kv, stream, _window_sizes(index, B * s_q, H)[1], torch.uint8)
     else:
         _expect("workspace", workspace, index, torch.uint8, None)
     if out is None:
-        out = q_nope.new_empty((B, s_q, H, 512))
+        out = _new(q_nope, stream, (B, s_q, H, 512), bf16)
     else:
         _expect("out", out, index, bf16, (B, s_q, H, 512))
     if lse is None:
-        lse = q_nope.new_empty((B, s_q, H), dtype=torch.float32)
+        lse = _new(q_nope, stream, (B, s_q, H), torch.float32)
     else:
         _expect("lse", lse, index, torch.float32, (B, s_q, H))
     code = getattr(_lib or load_library(), fn)(
         q_nope.data_ptr(), q_pe.data_ptr(), kv.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks,
         cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, softmax_scale, window, sinks, metadata.data_ptr(),
         4 * metadata.numel(), workspace.data_ptr(), workspace.numel(), out.data_ptr(), lse.data_ptr(), _ptr(status),
-        _launch_stream(index, stream))
+        handle)
     if code:
         raise MLAError(fn, code)
     return out, lse

@@ -10,11 +10,9 @@
 //        2^-2 (2^-10 of the row's maximum) and off by at most 2^-10 below that.  k' splits
 //        the same way into [k'_hi | k'_lo], a fifth 128-wide chunk beside the four of codes,
 //        against [q_hi | q_hi] and [q_lo | q_lo].
-//   PV:  P = 2^(x - m) * f = P_hi + P_lo with f = s * scale * log2 e, the key's factor in
-//        its score x, too (the epilogue divides it out of the constant), and m the running
-//        maximum of x + log2 f, lazily: P stays in [0, 2^8.6] and the terms' smallest step
-//        is 2^-14 of the largest weight s 2^x or finer, whatever the scales are.  The
-//        normaliser l = sum 2^(x - m) is fp32.
+//   PV:  P = 2^(x - m) * s = P_hi + P_lo, m the running maximum of x + log2 s, lazily: P stays
+//        in [0, 2^8.6] and the terms' smallest step is 2^-14 of the largest weight s 2^x or
+//        finer, whatever the scales are.  The normaliser l = sum 2^(x - m) is fp32.
 // Two 8-bit MMAs take the time of one bf16 MMA, so this costs no tensor time over the bf16
 // cache, moves half its bytes through the ring, and converts nothing but the 64 rotary
 // values a key.
@@ -74,9 +72,9 @@ constexpr uint32_t kTmemO = 0, kTmemS0 = 256, kTmemCols = 512;
 constexpr float kHeadroom = 5.0f, kRescaleThreshold = 3.5f;
 constexpr float kLogUnit = 0x1p15f;
 constexpr float kBias = kHeadroom + 383.0f;  // the logarithm read off the bits is 383 high
-// Factors below this count as it: a row of zeros (scale 0) still weighs 2^x in the
-// normaliser, and 2^x is kept in units of the largest x + log2 factor.
-constexpr float kMinFactor = 0x1p-100f;
+// Scales below this count as it: a row of zeros (scale 0) still weighs 2^x in the
+// normaliser, and 2^x is kept in units of the largest x + log2 s.
+constexpr float kMinScale = 0x1p-100f;
 constexpr int kMaxUp = 100;  // largest power of two of a query row
 constexpr uint32_t kIdescQK = make_idesc_e4m3(128, 256, false, false);
 constexpr uint32_t kIdescPV = make_idesc_e4m3(128, 256, false, true);
@@ -699,7 +697,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t buf = qk_count & 1;
           ok = wait_bar(&ctrl, p, smem_u32(&ctrl.sc_full[buf]), (qk_count >> 1) & 1) && ok;
           ok = wait_bar(&ctrl, p, smem_u32(&ctrl.s_full[buf]), (qk_count >> 1) & 1) && ok;
-          if (t == 0) rs = ctrl.row_scale[npieces & 3][m];
+          // (at least the smallest normal number: times a hidden key's -inf it stays -inf)
+          if (t == 0) {
+            rs = ctrl.row_scale[npieces & 3][m] * p.scale_log2;
+            if (rs < 0x1p-126f) rs = 0x1p-126f;
+          }
           tc_fence_after();
           const uint32_t ts = tmem + kTmemS0 + 128 * buf + lane_off + 64 * g;
           // of this thread's block, keys [c0, c0 + cnt) are visible
@@ -710,9 +712,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           auto seen = [&](int c) -> bool { return (uint32_t)(c - c0) < (uint32_t)cnt; };
           const bool full = __all_sync(0xffffffffu, cnt == kBlockSize);
-          // x = S * 2^-j * f with the key's factor f = s * scale * log2 e; the maximum is of
-          // z = x + log2 f.  The table holds f and lg = 2^15 (log2 f + 383), the logarithm read
-          // off f's bits (at most 0.087 low); z is kept in lg's units.
+          // x = S * s * rs with the key's scale s and rs = 2^-j * scale * log2 e; the maximum is
+          // of z = x + log2 s.  The table holds s and lg = 2^15 (log2 s + 383), the logarithm
+          // read off s's bits (at most 0.087 low); z is kept in lg's units.
           const float4* tab = reinterpret_cast<const float4*>(smem + kSmemTab + buf * kTabBytes) + 16 * (2 * hk + g);
           uint32_t sr[32];
           // scores of the 32 keys from c on (hidden ones -inf, whose weight 2^-inf is 0)
@@ -869,8 +871,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool bad = ctrl.bad_piece != 0;
         const float nanf_ = __int_as_float(0x7fc00000);
         // NaN scales make the row NaN; so does a NaN among the visible scores (l is NaN then)
-        // (the factors in P carry scale * log2 e beside s)
-        pend_sc = (bad || l_row != l_row) ? nanf_ : ((l_row > 0.f) ? 1.f / (l_row * p.scale_log2) : 0.f);
+        pend_sc = (bad || l_row != l_row) ? nanf_ : ((l_row > 0.f) ? 1.f / l_row : 0.f);
         pend_lse = (bad || l_row != l_row)
                        ? nanf_
                        : ((l_row > 0.f) ? (m_used * (1.0f / kLogUnit) - kBias + __log2f(l_row)) * 0.69314718055994531f : -INFINITY);
@@ -1002,8 +1003,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       };
       auto table_entry = [&](float* tab, int key, float s, bool seen) {
-        float f = seen ? s * p.scale_log2 : 1.0f;  // a hidden key's scale may be anything
-        if (f < kMinFactor) f = kMinFactor;        // a NaN stays one
+        float f = seen ? s : 1.0f;         // a hidden key's scale may be anything
+        if (f < kMinScale) f = kMinScale;  // a NaN stays one
         tab[key] = f;
         tab[kTileKeys + key] = (float)(__float_as_int(f) >> 8) + 0x1p23f;
       };

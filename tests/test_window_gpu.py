@@ -152,10 +152,11 @@ def test_a_key_reaches_only_the_tokens_that_see_it():
         assert torch.equal(o[0, 1 - hit], out[0, 1 - hit]) and torch.equal(l[0, 1 - hit], lse[0, 1 - hit])
 
 
+@pytest.mark.parametrize("units", [(60, 4, 16), (300, 3, 128), (500, 3, 128)])  # one pass of the scheduler, and several
 @pytest.mark.parametrize("window,sinks", [(64, 0), (500, 70), (1 << 20, 0)])
-def test_window_schedule_matches_oracle(window, sinks):
+def test_window_schedule_matches_oracle(window, sinks, units):
     rng = np.random.default_rng(9)
-    B, s_q, H = 300, 3, 128
+    B, s_q, H = units
     lens, q_lens = rng.integers(-1, 6000, size=B), rng.integers(-1, s_q + 2, size=B)
     meta = mla.get_metadata_window(i32(lens), i32(q_lens), s_q, H, window, sinks).cpu().numpy()
     keys = np.zeros(B * s_q, dtype=np.int64)  # 64 keys for each visible block
@@ -308,3 +309,95 @@ def test_serving_steps_together(fp8):
         compare(f64(out), lse.cpu().double().numpy(), ref, ref_lse, what="step")
         ref_y = O.absorb_out_ref(f64(out), O.bf16_to_f64(w_uv))
         assert np.all(np.abs(f64(y) - ref_y) <= 2.0 ** -8 * np.abs(ref_y) + 1e-4)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_nan_or_infinite_query_row_stays_alone(fp8):
+    p = Problem([500, 300, 70], 2, 64, 100, 70, seed=14)
+    good, good_lse = (x.clone() for x in p.run(fp8))
+    p.q_nope[0, 1, 5, 17], p.q_pe[2, 0, 63, 3], p.q_nope[1, 0, 9, 0] = 0x7FC0, 0x7FFF, 0x7F80
+    out, lse = p.run(fp8)
+    hit = torch.zeros(3, 2, 64, dtype=torch.bool, device="cuda")
+    hit[0, 1, 5] = hit[2, 0, 63] = hit[1, 0, 9] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], good[~hit]) and torch.equal(lse[~hit], good_lse[~hit])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("scale", [1e-30, 1e-6, 1.0])
+def test_softmax_scales(fp8, scale):
+    """From equal weights (the mean of the visible rows) to one key taking nearly all."""
+    p = Problem([700, 130], 1, 16, 200, 3, seed=15)
+    meta = mla.get_metadata_window(i32(p.lens), None, 1, 16, 200, 3)
+    cache = torch.from_numpy(p.packed()).cuda() if fp8 else dev(p.kv)
+    fn = mla.decode_fp8_window if fp8 else mla.decode_window
+    out, lse = fn(dev(p.q_nope), dev(p.q_pe), cache, i32(p.table), i32(p.lens), None, scale, 200, 3, meta)
+    ref, ref_lse = S.window_decode_ref(O.bf16_to_f64(p.q_nope), O.bf16_to_f64(p.q_pe), p.rows_of(fp8), p.lens, None,
+                                       scale, 200, 3)
+    compare(out.float().cpu().double().numpy(), lse.cpu().double().numpy(), ref, ref_lse, what=f"scale {scale}")
+
+
+def test_fp8_rows_of_very_different_scales():
+    """Rows 2^-60 to 2^6 of the others' size, rows of zeros, and zero queries: each row's scale
+    rides with its weight.  Weights are held to 2^-8 or 2^-14 of the largest s 2^x, so each
+    output is held to 2^-7 sum_t w_t |c_t| / sum_t w_t and what 1e-3 of the largest row adds."""
+    p = Problem([600, 90], 1, 16, 300, 64, seed=16)
+    rng = np.random.default_rng(17)
+    exp = rng.choice([-60, -20, -6, 0, 0, 0, 3, 6], size=p.kv.shape[:2])
+    values = O.bf16_to_f64(p.kv) * np.exp2(exp)[..., None]
+    values[rng.random(p.kv.shape[:2]) < 0.1] = 0
+    p.kv = np.where(np.isnan(values), p.kv, f32_to_bf16_bits(values.astype(np.float32)))
+    p.q_nope[0, 0, 3], p.q_pe[0, 0, 3] = 0, 0
+    out, lse = p.run(True)
+    got, got_lse = out.float().cpu().double().numpy(), lse.cpu().double().numpy()
+    ref, ref_lse = p.reference(True)
+    rows = p.rows_of(True)
+    for b, i, pos in S.new_tokens(p.lens, None, 1):
+        r = rows(b, S.window_keys(pos, 300, 64))
+        q = np.concatenate([O.bf16_to_f64(p.q_nope[b, i]), O.bf16_to_f64(p.q_pe[b, i])], -1)
+        w = np.exp(SCALE_192 * (q @ r.T) - ref_lse[b, i][:, None])
+        contrib = w[:, :, None] * np.abs(r[None, :, :512])
+        lim = 2.0 ** -7 * contrib.sum(1) + 1e-3 * contrib.max((1, 2))[:, None] + 2.0 ** -8 * np.abs(ref[b, i])
+        assert np.all(np.abs(got[b, i] - ref[b, i]) <= lim)
+    assert np.abs(got_lse - ref_lse).max() <= 1e-3
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_window_wait_timeout_sets_status_and_returns(fp8):
+    """The MMA warp waits on a barrier nothing completes (a test hook), bounded by 1 ms; every
+    role stops at its next bounded wait, the pair drains and returns, and the next call is
+    exact."""
+    p = Problem([3000, 700, 5000], 2, 128, 1024, 100, seed=18)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    try:
+        mla.set_wait_timeout_ns(1_000_000)
+        mla.set_stall_injection(True)
+        p.run(fp8, status)
+        torch.cuda.synchronize()
+    finally:
+        mla.set_stall_injection(False)
+        mla.set_wait_timeout_ns(0)
+    assert int(status.item()) & mla.MLA_DEVICE_ERR_TIMEOUT
+    p.check(fp8)
+
+
+def test_window_with_the_callers_buffers_and_stream_argument():
+    """Every tensor given, on a stream given; and nothing given but the stream."""
+    p = Problem([900, 64, 300], 2, 32, 128, 4, [2, 1, 2], seed=19)
+    want, want_lse = p.run()
+    n, ql, table, cache = i32(p.lens), i32(p.q_lens), i32(p.table), dev(p.kv)
+    qn, qp = dev(p.q_nope), dev(p.q_pe)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    meta = torch.empty(mla.metadata_size(6, 1, 32) // 4, dtype=torch.int32, device="cuda")
+    ws = torch.empty(mla.workspace_size(6, 1, 32), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+    s.wait_stream(torch.cuda.current_stream())
+    mla.get_metadata_window(n, ql, 2, 32, 128, 4, metadata=meta, stream=s)
+    got = mla.decode_window(qn, qp, cache, table, n, ql, SCALE_192, 128, 4, meta, workspace=ws, out=out, lse=lse, stream=s)
+    assert got[0] is out and got[1] is lse
+    m2 = mla.get_metadata_window(n, ql, 2, 32, 128, 4, stream=s)
+    out2, lse2 = mla.decode_window(qn, qp, cache, table, n, ql, SCALE_192, 128, 4, m2, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert torch.equal(out2, want) and torch.equal(lse2, want_lse)
