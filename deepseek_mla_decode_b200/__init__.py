@@ -485,13 +485,14 @@ def _torch_module():
     return _torch
 
 
-# The calls of a decode step take 2-5 us on the device, so the checks below are kept to
-# attribute reads and tuple comparisons (about 0.3 us a tensor).
-def _expect(name, t, index, dtype, shape):
-    """t must be a contiguous tensor of dtype and shape (None: any) on CUDA device `index`."""
+# The calls of a decode step take 2-5 us on the device, so their checks are inlined comparisons
+# (about 0.2 us a tensor) and _expect only words the refusal.
+def _expect(name, t, index, dtype, shape=None):
+    """Refuses t if it is not a contiguous tensor of dtype and shape (None: any) on CUDA
+    device `index`."""
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
@@ -504,17 +505,17 @@ def _device_index(t):
     index = t.get_device()
     if index < 0:
         raise ValueError("CUDA tensors expected")
-    if index != _torch.cuda.current_device():
+    if index != _torch._C._cuda_getDevice():
         raise ValueError(f"tensors are on cuda:{index}, the current device is cuda:{_torch.cuda.current_device()}")
     return index
 
 
-def _new(like, stream, shape, dtype):
-    """An uninitialised tensor for a launch on `stream`.  It comes from that stream's memory
+def _new(like, stream, shape, dtype=None):
+    """An uninitialised tensor (None: of like's dtype) for a launch on `stream`.  It comes from that stream's memory
     pool: memory of the current stream's pool may still be in use there, and a workspace goes
     back to its pool before the kernels that use it have run."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
     with _torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
@@ -529,13 +530,19 @@ def _launch_stream(index, stream):
 
 
 def _tokens(index, B, cache_seqlens, q_lens, status):
-    """Checks the per-sequence words of a call."""
-    i32 = _torch.int32
-    _expect("cache_seqlens", cache_seqlens, index, i32, (B,))
+    """Checks the per-sequence words of a call; returns the pointers of q_lens and status."""
+    i32, shape = _torch.int32, (B,)
+    n = cache_seqlens
+    if n.shape != shape or n.dtype is not i32 or n.get_device() != index or not n.is_contiguous():
+        _expect("cache_seqlens", n, index, i32, shape)
     if q_lens is not None:
-        _expect("q_lens", q_lens, index, i32, (B,))
+        if q_lens.shape != shape or q_lens.dtype is not i32 or q_lens.get_device() != index or not q_lens.is_contiguous():
+            _expect("q_lens", q_lens, index, i32, shape)
+        q_lens = q_lens.data_ptr()
     if status is not None:
-        _expect("status", status, index, i32, None)
+        _expect("status", status, index, i32)
+        status = status.data_ptr()
+    return q_lens, status
 
 
 def _token_rows(name, t, inner, width):
@@ -560,34 +567,30 @@ def _window_sizes(index, units, H):
     return metadata_size(units, 1, H), workspace_size(units, 1, H)
 
 
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
-
-
 def rope_q(q, cache_seqlens, rope: Rope, q_lens=None, q_heads=None, q_pe=None, status=None, stream=None):
     """mla_rope_q: splits query heads q [B, s_q, H, 192] = [128 | 64 rotary] into q_heads
     [B, s_q, H, 128] (for absorb_q) and q_pe [B, s_q, H, 64] (for decode), the latter rotated
     at each token's position.  q may be a column slice of a wider projection."""
-    torch = _torch or _torch_module()
-    bf16 = torch.bfloat16
-    if q.dim() != 4 or q.shape[3] != 192 or q.dtype != bf16:
+    bf16 = (_torch or _torch_module()).bfloat16
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != 192 or q.dtype is not bf16:
         raise ValueError("bf16 q [B, s_q, H, 192] expected")
-    B, s_q, H, _ = q.shape
-    row = _token_rows("q", q, (192, 1), H * 192)
+    B, s_q, H, _ = shape
+    row = H * 192 if q.is_contiguous() else _token_rows("q", q, (192, 1), H * 192)
     index = _device_index(q)
     handle = _launch_stream(index, stream)
-    _tokens(index, B, cache_seqlens, q_lens, status)
+    ql, st = _tokens(index, B, cache_seqlens, q_lens, status)
     if q_heads is None:
-        q_heads = _new(q, stream, (B, s_q, H, 128), bf16)
+        q_heads = _new(q, stream, (B, s_q, H, 128))
     else:
         _expect("q_heads", q_heads, index, bf16, (B, s_q, H, 128))
     if q_pe is None:
-        q_pe = _new(q, stream, (B, s_q, H, 64), bf16)
+        q_pe = _new(q, stream, (B, s_q, H, 64))
     else:
         _expect("q_pe", q_pe, index, bf16, (B, s_q, H, 64))
     code = (_lib or load_library()).mla_rope_q(
-        q.data_ptr(), row, cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, rope, q_heads.data_ptr(),
-        q_pe.data_ptr(), _ptr(status), handle)
+        q.data_ptr(), row, cache_seqlens.data_ptr(), ql, B, s_q, H, rope, q_heads.data_ptr(), q_pe.data_ptr(), st,
+        handle)
     if code:
         raise MLAError("mla_rope_q", code)
     return q_heads, q_pe
@@ -597,37 +600,44 @@ def rope_inplace(q, cache_seqlens, rope: Rope, q_lens=None, status=None, stream=
     """mla_rope_inplace: rotates the last 64 of each head of q [B, s_q, H, 192] where they
     lie; returns q."""
     torch = _torch or _torch_module()
-    if q.dim() != 4 or q.shape[3] != 192 or q.dtype != torch.bfloat16:
+    if q.dim() != 4 or q.shape[3] != 192 or q.dtype is not torch.bfloat16:
         raise ValueError("bf16 q [B, s_q, H, 192] expected")
     B, s_q, H, _ = q.shape
-    row = _token_rows("q", q, (192, 1), H * 192)
+    row = H * 192 if q.is_contiguous() else _token_rows("q", q, (192, 1), H * 192)
     index = _device_index(q)
     handle = _launch_stream(index, stream)
-    _tokens(index, B, cache_seqlens, q_lens, status)
+    ql, st = _tokens(index, B, cache_seqlens, q_lens, status)
     _check("mla_rope_inplace", (_lib or load_library()).mla_rope_inplace(
-        q.data_ptr(), row, cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, rope, _ptr(status), handle))
+        q.data_ptr(), row, cache_seqlens.data_ptr(), ql, B, s_q, H, rope, st, handle))
     return q
 
 
 def _append(fn, kv_a, cache, width, dtype, block_table, cache_seqlens, rope, norm_weight, eps, q_lens, status, stream):
-    if kv_a.dim() != 3 or kv_a.shape[2] != 576 or kv_a.dtype != _torch.bfloat16:
+    bf16, i32 = _torch.bfloat16, _torch.int32
+    shape, pool, table = kv_a.shape, cache.shape, block_table.shape
+    if len(shape) != 3 or shape[2] != 576 or kv_a.dtype is not bf16:
         raise ValueError("bf16 kv_a [B, s_q, 576] expected")
-    if cache.dim() != 3 or cache.shape[1:] != (64, width):
+    if len(pool) != 3 or pool[1:] != (64, width):
         raise ValueError(f"cache [num_blocks, 64, {width}] expected")
-    if block_table.dim() != 2:
+    B, s_q, _ = shape
+    if len(table) != 2 or table[0] != B:
         raise ValueError("block_table [B, max_blocks] expected")
-    B, s_q, _ = kv_a.shape
-    row = _token_rows("kv_a", kv_a, (1,), 576)
+    row = 576 if kv_a.is_contiguous() else _token_rows("kv_a", kv_a, (1,), 576)
     index = _device_index(kv_a)
-    max_blocks = block_table.shape[1]
-    _tokens(index, B, cache_seqlens, q_lens, status)
-    _expect("cache", cache, index, dtype, None)
-    _expect("block_table", block_table, index, _torch.int32, (B, max_blocks))
+    handle = _launch_stream(index, stream)
+    ql, st = _tokens(index, B, cache_seqlens, q_lens, status)
+    if cache.dtype is not dtype or cache.get_device() != index or not cache.is_contiguous():
+        _expect("cache", cache, index, dtype)
+    if block_table.dtype is not i32 or block_table.get_device() != index or not block_table.is_contiguous():
+        _expect("block_table", block_table, index, i32)
     if norm_weight is not None:
-        _expect("norm_weight", norm_weight, index, _torch.bfloat16, (512,))
+        w = norm_weight
+        if w.shape != (512,) or w.dtype is not bf16 or w.get_device() != index or not w.is_contiguous():
+            _expect("norm_weight", w, index, bf16, (512,))
+        norm_weight = w.data_ptr()
     code = getattr(_lib or load_library(), fn)(
-        kv_a.data_ptr(), row, _ptr(norm_weight), eps, block_table.data_ptr(), max_blocks, cache_seqlens.data_ptr(),
-        _ptr(q_lens), B, s_q, rope, cache.data_ptr(), cache.shape[0], _ptr(status), _launch_stream(index, stream))
+        kv_a.data_ptr(), row, norm_weight, eps, block_table.data_ptr(), table[1], cache_seqlens.data_ptr(), ql, B, s_q,
+        rope, cache.data_ptr(), pool[0], st, handle)
     if code:
         raise MLAError(fn, code)
     return cache
@@ -654,54 +664,60 @@ def append_kv_fp8(kv_a, kv_fp8, block_table, cache_seqlens, rope: Optional[Rope]
 def get_metadata_window(cache_seqlens, q_lens, s_q: int, H: int, window: int, sinks: int, metadata=None, stream=None):
     """mla_get_metadata_window: the schedule for decode_window / decode_fp8_window (shared by
     every layer of a step); q_lens may be None."""
-    torch = _torch or _torch_module()
+    i32 = (_torch or _torch_module()).int32
     (B,) = cache_seqlens.shape
     index = _device_index(cache_seqlens)
     handle = _launch_stream(index, stream)
-    _tokens(index, B, cache_seqlens, q_lens, None)
+    ql, _ = _tokens(index, B, cache_seqlens, q_lens, None)
     if metadata is None:
-        metadata = _new(cache_seqlens, stream, _window_sizes(index, B * s_q, H)[0] // 4, torch.int32)
+        metadata = _new(cache_seqlens, stream, _window_sizes(index, B * s_q, H)[0] // 4)
     else:
-        _expect("metadata", metadata, index, torch.int32, None)
-    _check("mla_get_metadata_window", (_lib or load_library()).mla_get_metadata_window(
-        cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, window, sinks, metadata.data_ptr(), 4 * metadata.numel(),
-        handle))
+        _expect("metadata", metadata, index, i32)
+    code = (_lib or load_library()).mla_get_metadata_window(
+        cache_seqlens.data_ptr(), ql, B, s_q, H, window, sinks, metadata.data_ptr(), 4 * metadata.numel(), handle)
+    if code:
+        raise MLAError("mla_get_metadata_window", code)
     return metadata
 
 
 def _decode_window(fn, q_nope, q_pe, kv, width, dtype, block_table, cache_seqlens, q_lens, softmax_scale, window, sinks,
                    metadata, workspace, out, lse, status, stream):
-    torch = _torch
-    if q_nope.dim() != 4 or kv.dim() != 3 or block_table.dim() != 2:
+    bf16, f32, i32 = _torch.bfloat16, _torch.float32, _torch.int32
+    shape, pool, table = q_nope.shape, kv.shape, block_table.shape
+    if len(shape) != 4 or len(pool) != 3 or len(table) != 2:
         raise ValueError("q_nope [B, s_q, H, 512], cache [num_blocks, 64, width], block_table [B, max_blocks] expected")
-    B, s_q, H, _ = q_nope.shape
-    bf16, i32 = torch.bfloat16, torch.int32
+    B, s_q, H, d = shape
     index = _device_index(q_nope)
     handle = _launch_stream(index, stream)
-    max_blocks, num_blocks = block_table.shape[1], kv.shape[0]
-    _expect("q_nope", q_nope, index, bf16, (B, s_q, H, 512))
-    _expect("q_pe", q_pe, index, bf16, (B, s_q, H, 64))
-    _expect("cache", kv, index, dtype, (num_blocks, 64, width))
-    _expect("block_table", block_table, index, i32, (B, max_blocks))
-    _expect("metadata", metadata, index, i32, None)
-    _tokens(index, B, cache_seqlens, q_lens, status)
+    if d != 512 or q_nope.dtype is not bf16 or not q_nope.is_contiguous():
+        _expect("q_nope", q_nope, index, bf16, (B, s_q, H, 512))
+    if (q_pe.shape != (B, s_q, H, 64) or q_pe.dtype is not bf16 or q_pe.get_device() != index
+            or not q_pe.is_contiguous()):
+        _expect("q_pe", q_pe, index, bf16, (B, s_q, H, 64))
+    if pool[1:] != (64, width) or kv.dtype is not dtype or kv.get_device() != index or not kv.is_contiguous():
+        _expect("cache", kv, index, dtype, (pool[0], 64, width))
+    if (table[0] != B or block_table.dtype is not i32 or block_table.get_device() != index
+            or not block_table.is_contiguous()):
+        _expect("block_table", block_table, index, i32, (B, table[1]))
+    if metadata.dtype is not i32 or metadata.get_device() != index or not metadata.is_contiguous():
+        _expect("metadata", metadata, index, i32)
+    ql, st = _tokens(index, B, cache_seqlens, q_lens, status)
     if workspace is None:
-        workspace = _new(kv, stream, _window_sizes(index, B * s_q, H)[1], torch.uint8)
+        workspace = _new(kv, stream, _window_sizes(index, B * s_q, H)[1], _torch.uint8)
     else:
-        _expect("workspace", workspace, index, torch.uint8, None)
+        _expect("workspace", workspace, index, _torch.uint8)
     if out is None:
-        out = _new(q_nope, stream, (B, s_q, H, 512), bf16)
+        out = _new(q_nope, stream, shape)
     else:
         _expect("out", out, index, bf16, (B, s_q, H, 512))
     if lse is None:
-        lse = _new(q_nope, stream, (B, s_q, H), torch.float32)
+        lse = _new(q_nope, stream, shape[:3], f32)
     else:
-        _expect("lse", lse, index, torch.float32, (B, s_q, H))
+        _expect("lse", lse, index, f32, (B, s_q, H))
     code = getattr(_lib or load_library(), fn)(
-        q_nope.data_ptr(), q_pe.data_ptr(), kv.data_ptr(), num_blocks, block_table.data_ptr(), max_blocks,
-        cache_seqlens.data_ptr(), _ptr(q_lens), B, s_q, H, softmax_scale, window, sinks, metadata.data_ptr(),
-        4 * metadata.numel(), workspace.data_ptr(), workspace.numel(), out.data_ptr(), lse.data_ptr(), _ptr(status),
-        handle)
+        q_nope.data_ptr(), q_pe.data_ptr(), kv.data_ptr(), pool[0], block_table.data_ptr(), table[1],
+        cache_seqlens.data_ptr(), ql, B, s_q, H, softmax_scale, window, sinks, metadata.data_ptr(),
+        4 * metadata.numel(), workspace.data_ptr(), workspace.numel(), out.data_ptr(), lse.data_ptr(), st, handle)
     if code:
         raise MLAError(fn, code)
     return out, lse
