@@ -7,6 +7,13 @@
 // scaled rotary keys come from the 32-bit row.  Memory-bound: 1152 bytes read and 1152 or
 // 656 written a row.
 //
+// Measured: 65536 rows with norm and rotation in 29.7 us, 5.1 TB/s, 78 % of a plain copy
+// (25.4 us without the two: instructions are issued in two cycles of three, so norm and
+// rotation still cost 4 us); 20 k FP8 rows in 14 us, whose 16 codes a lane are products
+// instead of divisions where that decides them (17.2 us with divisions); a decode step's 256
+// rows in 2.4 us, a launch.  Two rows a warp (30.5 us) and persistent warps that load a row
+// ahead (36 us) lose to more warps: 48 registers keep 40 of them on an SM.
+//
 // One warp per row.  Lane l holds c[8l..8l+7] and c[256+8l..256+8l+7] (two 16-byte loads,
 // and 8- or 16-byte stores, contiguous over the warp) and pair l of k; the sum of squares
 // and the row maximum are butterflies over the warp, in a fixed order.

@@ -23,6 +23,15 @@
 // and dims 256h + 128r + (0..127) as its half of the PV operand.  One box of the cache, 64
 // rows x 128 code bytes, serves both: K-major for QK, MN-major for PV.
 //
+// Measured (192 sequences, 128 heads, window 4096, attention and combine): 264-271 us on the
+// pool's boxes, 49 % of the tensor floor, against 432 us for the kernel that converts codes to
+// bf16.  No unit is busy half the time (tensor pipe 45 %, issue 39 %, DRAM 28 %); a tile of
+// 9.7 k cycles is the softmax's two passes (5 k), its hand-offs (3 k) and, spread over 13
+// tiles, the switch of pieces (0.9 k: the new query's terms and the old output).  The
+// instruction stream is part of it: with both passes unrolled over 64 keys and the terms made
+// by unrolled code the kernel took 346 us, for the warps waited for instructions; so passes
+// run over 32 keys twice and read the scores from tensor memory again.
+//
 // Warps: 0, 2, 3 producers, 1 MMA issue (leader) and TMEM, 4..11 softmax and epilogue,
 // 12..15 preparation (the query rows' terms once a piece; the rotary keys' terms and the
 // scale tables once a tile).
