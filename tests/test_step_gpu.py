@@ -72,6 +72,7 @@ def check_bf16(got, ref, slack, what):
     (3, 5, [9, 2, 0, 400], None),           # fewer cached tokens than new ones: no place
     (4, 33, [4, 100, 1000, 7], [4, 0, 2, 3]),
     (200, 1, [200, 131072], [200, 77]),
+    (700, 40, [700, 5000, -1, 3, 900], [700, 3, 1, 5, 701]),  # padding and invalid counts past the GPU's warps
 ])
 def test_rope_q(kw, s_q, H, lens, q_lens):
     q = bits((len(lens), s_q, H, 192), seed=H)
@@ -79,9 +80,14 @@ def test_rope_q(kw, s_q, H, lens, q_lens):
     heads, pe = mla.rope_q(dev(q), i32(lens), mla.rope_params(**kw), q_lens=None if q_lens is None else i32(q_lens),
                            status=status)
     x, rot = O.bf16_to_f64(q), oracle_rotation(kw)
-    ref_heads, ref_pe = S.rope_q_ref(x, lens, q_lens, **rot)
-    assert int(status.item()) == 0
-    assert np.array_equal(f64(heads), ref_heads)
+    bad = [n < 0 or (q_lens is not None and not 0 <= q_lens[b] <= s_q) for b, n in enumerate(lens)]
+    counts = None if q_lens is None else [0 if w else c for w, c in zip(bad, q_lens)]
+    ref_heads, ref_pe = S.rope_q_ref(x, lens, counts, **rot)
+    ref_heads[bad], ref_pe[bad] = np.nan, np.nan
+    assert int(status.item()) == (mla.MLA_DEVICE_ERR_SEQLEN if any(bad) else 0)
+    assert np.array_equal(f64(heads), ref_heads, equal_nan=True)
+    assert np.array_equal(np.isnan(f64(pe)), np.isnan(ref_pe))
+    ref_pe[bad], pe[bad] = 0, 0
     check_bf16(f64(pe), ref_pe, rope_slack(x[..., 128:], rot["half"], rot["amplitude"]) * (ref_pe != 0), "q_pe")
 
 
@@ -100,6 +106,16 @@ def test_rope_q_of_a_projection_slice_and_in_place(layout):
     want[..., 16:16 + H * 192].unflatten(-1, (H, 192))[..., 128:] = pe
     mla.rope_inplace(q, lens, r)
     assert torch.equal(wide, want)
+
+
+def test_rope_in_place_with_padding_past_the_gpus_warps():
+    q = dev(bits((4, 700, 33, 192), seed=9))
+    lens, q_lens, r = i32([700, 5000, -1, 3]), i32([700, 3, 1, 5]), mla.rope_params(layout="half")
+    _, pe = mla.rope_q(q, lens, r, q_lens=q_lens)
+    want = q.clone()
+    want[..., 128:] = pe
+    mla.rope_inplace(q, lens, r, q_lens=q_lens)
+    assert torch.equal(torch.nan_to_num(q, 777.0), torch.nan_to_num(want, 777.0))
 
 
 def test_rope_q_invalid_lengths_and_counts():
@@ -152,6 +168,7 @@ APPENDS = [
     (3, [9, 2, 0, 400], None),
     (4, [4, 100, 1000, 7], [4, 0, 2, 3]),
     (150, [150, 1000, 129], [150, 77, 129]),  # whole blocks and ragged ends
+    (2500, [2500, 3000, 100], [2500, 17, 100]),  # more rows than the GPU holds warps, most of them padding
 ]
 
 
