@@ -245,7 +245,6 @@ __device__ __forceinline__ bool wait_bar(Ctrl* c, const Params& p, uint32_t bar,
   }
 }
 
-
 // Four values as two e4m3 terms each: hi the value rounded to e4m3's four bits (an fp32 add
 // and mask: ties away, above the smallest normal), lo what that left.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -277,7 +276,10 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t* w) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t w;
@@ -293,6 +295,10 @@ __device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
+
+// ===========================================================================
+// the kernel
+// ===========================================================================
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     window_fp8_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -700,7 +706,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int bad_ids = 0;
         {
           const int32_t* bt = unit_table(p, pc.b);
-          for (int k = pc.k_lo + st; k < pc.k_hi; k += kNumSoftmaxThreads) bad_ids |= !valid_id(p, bt[window_block(pc.w, k)]);
+          for (int k = pc.k_lo + st; k < pc.k_hi; k += kNumSoftmaxThreads)
+            bad_ids |= !valid_id(p, bt[window_block(pc.w, k)]);
         }
         for (int t = 0; t < nt && go; ++t) {
           const uint32_t buf = qk_count & 1;
@@ -745,8 +752,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; i += 4) {
               const float4 f = tab[(c + i) >> 2], lg = tab[64 + ((c + i) >> 2)];
               float z0, z1, z2, z3;
-              unpack_f32x2(fma2(mul2(pack_f32x2(score(i), score(i + 1)), pack_f32x2(f.x, f.y)), rsz, pack_f32x2(lg.x, lg.y)), z0, z1);
-              unpack_f32x2(fma2(mul2(pack_f32x2(score(i + 2), score(i + 3)), pack_f32x2(f.z, f.w)), rsz, pack_f32x2(lg.z, lg.w)), z2, z3);
+              const uint64_t y01 = mul2(pack_f32x2(score(i), score(i + 1)), pack_f32x2(f.x, f.y));
+              const uint64_t y23 = mul2(pack_f32x2(score(i + 2), score(i + 3)), pack_f32x2(f.z, f.w));
+              unpack_f32x2(fma2(y01, rsz, pack_f32x2(lg.x, lg.y)), z0, z1);
+              unpack_f32x2(fma2(y23, rsz, pack_f32x2(lg.z, lg.w)), z2, z3);
               mx0 = max3(mx0, z0, z1);
               mx1 = max3(mx1, z2, z3);
             }
@@ -781,7 +790,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               float e0, e1, e2, e3;
               unpack_f32x2(fma2(mul2(pack_f32x2(score(4 * q), score(4 * q + 1)), f01), rs2, nref2), e0, e1);
               unpack_f32x2(fma2(mul2(pack_f32x2(score(4 * q + 2), score(4 * q + 3)), f23), rs2, nref2), e2, e3);
-              const uint64_t e01 = pack_f32x2(fast_exp2(e0), fast_exp2(e1)), e23 = pack_f32x2(fast_exp2(e2), fast_exp2(e3));
+              const uint64_t e01 = pack_f32x2(fast_exp2(e0), fast_exp2(e1));
+              const uint64_t e23 = pack_f32x2(fast_exp2(e2), fast_exp2(e3));
               l01 = add2(l01, e01);
               l23 = add2(l23, e23);
               unpack_f32x2(mul2(e01, f01), e0, e1);
@@ -881,9 +891,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float nanf_ = __int_as_float(0x7fc00000);
         // NaN scales make the row NaN; so does a NaN among the visible scores (l is NaN then)
         pend_sc = (bad || l_row != l_row) ? nanf_ : ((l_row > 0.f) ? 1.f / l_row : 0.f);
-        pend_lse = (bad || l_row != l_row)
-                       ? nanf_
-                       : ((l_row > 0.f) ? (m_used * (1.0f / kLogUnit) - kBias + __log2f(l_row)) * 0.69314718055994531f : -INFINITY);
+        const float lse2 = m_used * (1.0f / kLogUnit) - kBias + __log2f(l_row);
+        pend_lse = (bad || l_row != l_row) ? nanf_ : ((l_row > 0.f) ? lse2 * 0.69314718055994531f : -INFINITY);
         pend_direct = (nsplit == 1);
         pend_b = pc.b;
         pend_slot = split_base + pc.split;
@@ -990,6 +999,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int idA = 0, idB = 0;                // blocks of those two keys
       bool seenA = false, seenB = false;   // whether they are visible
       const int r = pt & 63;
+      auto scale_of = [&](int id) -> float {
+        const uint8_t* row = p.rows + ((int64_t)id * kBlockSize + r) * kRowBytes8;
+        return __ldg(reinterpret_cast<const float*>(row + kOffScale8));
+      };
       auto load_tile = [&](const Piece& pc, const int32_t* bt, int t) {
         const int nb = blocks_in_tile(pc, t), v0 = pc.k_lo + t * kBlocksPerTile, kb = pt >> 6;
         seenA = seenB = false;
@@ -1000,7 +1013,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           int lo, hi;
           rows_in_block(pc, t, kb, &lo, &hi);
           seenA = r >= lo && r < hi;
-          sA = __ldg(reinterpret_cast<const float*>(p.rows + ((int64_t)idA * kBlockSize + r) * kRowBytes8 + kOffScale8));
+          sA = scale_of(idA);
         }
         if (kb + 2 < nb) {
           const int32_t id = bt[window_block(pc.w, v0 + kb + 2)];
@@ -1008,7 +1021,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           int lo, hi;
           rows_in_block(pc, t, kb + 2, &lo, &hi);
           seenB = r >= lo && r < hi;
-          sB = __ldg(reinterpret_cast<const float*>(p.rows + ((int64_t)idB * kBlockSize + r) * kRowBytes8 + kOffScale8));
+          sB = scale_of(idB);
         }
       };
       auto table_entry = [&](float* tab, int key, float s, bool seen) {
@@ -1052,7 +1065,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (pw == 0 && __all_sync(0xffffffffu, ok)) load_q(cur.b);
         load_tile(cur, bt, 0);
         ok = wait_bar(&ctrl, p, smem_u32(&ctrl.q_raw), npieces & 1) && ok;
-        if (ok) split_rows(npieces);
+        if (__all_sync(0xffffffffu, ok)) split_rows(npieces);  // (whole warps: it shuffles)
         if (!publish()) break;
         if (pt == 0) arrive(&ctrl.q_full, q_full_l);
         const int nt = num_tiles(cur);
