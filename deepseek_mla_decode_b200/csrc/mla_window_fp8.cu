@@ -29,8 +29,8 @@
 // 9.7 k cycles is the softmax's two passes (5 k), its hand-offs (3 k) and, spread over 13
 // tiles, the switch of pieces (0.9 k: the new query's terms and the old output).  The
 // instruction stream is part of it: with both passes unrolled over 64 keys and the terms made
-// by unrolled code the kernel took 346 us, for the warps waited for instructions; so passes
-// run over 32 keys twice and read the scores from tensor memory again.
+// by unrolled code the kernel took 346 us, for the warps waited for instructions; so the
+// passes run over groups of 16 and 32 keys and read the scores from tensor memory twice.
 //
 // Warps: 0, 2, 3 producers, 1 MMA issue (leader) and TMEM, 4..11 softmax and epilogue,
 // 12..15 preparation (the query rows' terms once a piece; the rotary keys' terms and the
@@ -732,28 +732,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // of z = x + log2 s.  The table holds s and lg = 2^15 (log2 s + 383), the logarithm
           // read off s's bits (at most 0.087 low); z is kept in lg's units.
           const float4* tab = reinterpret_cast<const float4*>(smem + kSmemTab + buf * kTabBytes) + 16 * (2 * hk + g);
-          uint32_t sr[32];
-          // scores of the 32 keys from c on (hidden ones -inf, whose weight 2^-inf is 0)
-          auto load_scores = [&](int c) {
-            tmem_ld32_wait(ts + c, sr);
+          // hidden keys of a group that starts at key c score -inf: their weight is 2^-inf = 0
+          auto hide = [&](uint32_t* s, int c, int count) {
             if (!full) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!seen(c + i)) sr[i] = 0xff800000u;
+              for (int i = 0; i < count; ++i)
+                if (!seen(c + i)) s[i] = 0xff800000u;
             }
           };
-          auto score = [&](int i) -> float { return __uint_as_float(sr[i]); };
+          auto score = [](uint32_t s) -> float { return __uint_as_float(s); };
           float mx0 = -INFINITY, mx1 = -INFINITY;
           const uint64_t rsz = pack_f32x2(rs * kLogUnit, rs * kLogUnit);
 #pragma unroll 1
-          for (int c = 0; c < 64; c += 32) {
-            load_scores(c);
+          for (int c = 0; c < 64; c += 16) {
+            uint32_t s[16];
+            tmem_ld16_wait(ts + c, s);
+            hide(s, c, 16);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
+            for (int i = 0; i < 16; i += 4) {
               const float4 f = tab[(c + i) >> 2], lg = tab[64 + ((c + i) >> 2)];
+              const uint64_t y01 = mul2(pack_f32x2(score(s[i]), score(s[i + 1])), pack_f32x2(f.x, f.y));
+              const uint64_t y23 = mul2(pack_f32x2(score(s[i + 2]), score(s[i + 3])), pack_f32x2(f.z, f.w));
               float z0, z1, z2, z3;
-              const uint64_t y01 = mul2(pack_f32x2(score(i), score(i + 1)), pack_f32x2(f.x, f.y));
-              const uint64_t y23 = mul2(pack_f32x2(score(i + 2), score(i + 3)), pack_f32x2(f.z, f.w));
               unpack_f32x2(fma2(y01, rsz, pack_f32x2(lg.x, lg.y)), z0, z1);
               unpack_f32x2(fma2(y23, rsz, pack_f32x2(lg.z, lg.w)), z2, z3);
               mx0 = max3(mx0, z0, z1);
@@ -782,14 +782,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 64; c += 32) {
 #pragma unroll
             for (int q = 0; q < 16; ++q) pa[q] = pb[q];
-            load_scores(c);
+            uint32_t s[32];
+            tmem_ld32_wait(ts + c, s);
+            hide(s, c, 32);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
               const float4 f = tab[(c >> 2) + q];
               const uint64_t f01 = pack_f32x2(f.x, f.y), f23 = pack_f32x2(f.z, f.w);
               float e0, e1, e2, e3;
-              unpack_f32x2(fma2(mul2(pack_f32x2(score(4 * q), score(4 * q + 1)), f01), rs2, nref2), e0, e1);
-              unpack_f32x2(fma2(mul2(pack_f32x2(score(4 * q + 2), score(4 * q + 3)), f23), rs2, nref2), e2, e3);
+              unpack_f32x2(fma2(mul2(pack_f32x2(score(s[4 * q]), score(s[4 * q + 1])), f01), rs2, nref2), e0, e1);
+              unpack_f32x2(fma2(mul2(pack_f32x2(score(s[4 * q + 2]), score(s[4 * q + 3])), f23), rs2, nref2), e2, e3);
               const uint64_t e01 = pack_f32x2(fast_exp2(e0), fast_exp2(e1));
               const uint64_t e23 = pack_f32x2(fast_exp2(e2), fast_exp2(e3));
               l01 = add2(l01, e01);
