@@ -171,16 +171,16 @@ mla_status_t rope_q_any(const void* q, int64_t row_stride, const int32_t* cache_
 }  // namespace
 
 bool rope_turns(const mla_rope_t* rope, RopeTurns* out) {
-  constexpr long double kTwoPi = 6.283185307179586476925286766559L;
+  constexpr long double kTurn = 1.0L / 6.283185307179586476925286766559L;
   if (rope->half_layout != 0 && rope->half_layout != 1) return false;
   if (!std::isfinite(rope->amplitude)) return false;
   for (int i = 0; i < kDRope / 2; ++i) {
     // beyond this extended precision keeps too little of a turn's fraction
     if (!(std::fabs(rope->freq[i]) <= 1e6)) return false;
-    long double t = rope->freq[i] / kTwoPi;
-    t -= std::floor(t);
-    t *= 18446744073709551616.0L;
-    out->turns[i] = t >= 18446744073709551615.0L ? 0u : static_cast<uint64_t>(t);
+    // whole turns of either sign drop out, and the fraction is kept to 2^-63 of a turn
+    long double t = rope->freq[i] * kTurn;
+    t -= static_cast<long double>(static_cast<int64_t>(t));
+    out->turns[i] = static_cast<uint64_t>(static_cast<int64_t>(t * 0x1p63L)) << 1;
   }
   out->amplitude = rope->amplitude;
   return true;
