@@ -39,12 +39,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
 // kColParts warps per query row, each over 512 / kColParts columns; kGroup partial rows
 // in flight per lane (32 registers of loads for one warp per row and two splits, 64 for
 // four warps per row and sixteen splits); kBySeq: block x is a sequence (else a
-// partition)
-template <int kColParts, int kGroup, bool kBySeq>
-__global__ void __launch_bounds__(kWarps * 32) combine_kernel(
+// partition); kWin: of a windowed schedule.  The one-warp kernels are held to 64 registers
+// (four blocks on an SM: with 76 the merge of 64 sequences took 1.1 us longer)
+template <int kColParts, int kGroup, bool kBySeq, bool kWin>
+__global__ void __launch_bounds__(kWarps * 32, kColParts == 1 ? 4 : 2) combine_kernel(
     const int32_t* __restrict__ meta, const int32_t* __restrict__ seqlens, const int32_t* __restrict__ q_lens,
-    int max_blocks, int B, int s_q, int M, const float* __restrict__ part_o, const float* __restrict__ part_lse,
-    __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int tok_rep, int tok_causal, int window, int sinks) {
+    int max_blocks, int B, int s_q, int M, uint64_t signature, const float* __restrict__ part_o,
+    const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int tok_rep,
+    int tok_causal, int window, int sinks) {
   // launched as a programmatic dependent of the attention kernel: wait for it
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // Dependent round trips to memory: the partition's start (by partition only), then
@@ -60,6 +62,7 @@ __global__ void __launch_bounds__(kWarps * 32) combine_kernel(
     const int k0 = meta[off_part_start() + 2 * part + 1];
     if (b >= B || k0 == 0) return;  // partition opens a sequence (or is empty)
   }
+  const bool ours = *reinterpret_cast<const uint64_t*>(meta + kHdrSignature) == signature;
   const int fp = meta[off_first_part(B) + b];
   const int nblk = meta[off_nblk() + b];
   const int ns = meta[off_num_splits(B) + b];
@@ -75,13 +78,13 @@ __global__ void __launch_bounds__(kWarps * 32) combine_kernel(
                                                                                             tok_causal));
   const int ql = tok_rep ? 1 : qr;
   if constexpr (kBySeq) {
-    if (ns < 2) return;  // one piece: its rows were written by the attention kernel
+    if (ns < 2 || !ours) return;  // one piece: its rows were written by the attention kernel
   } else {
-    if (fp + 1 != part) return;  // a later cut of the same sequence
+    if (fp + 1 != part || !ours) return;  // a later cut of the same sequence
   }
   // rows written as NaN already: invalid length, or a schedule built for another length
   if (n < 0 || (int64_t)n > (int64_t)max_blocks * kBlockSize) return;
-  if (nblk != (window > 0 ? window_blocks(n, window, sinks).count : (n + kBlockSize - 1) / kBlockSize)) return;
+  if (nblk != (kWin ? window_blocks(n, window, sinks).count : (n + kBlockSize - 1) / kBlockSize)) return;
   if (ql < 0 || ql > s_q) return;  // invalid query count: NaN rows written already
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wid = blockIdx.y * kWarps + warp;
@@ -180,14 +183,14 @@ cudaError_t launch_combine(const int32_t* meta, const int32_t* seqlens, const in
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out);
-  if (wide)
-    return cudaLaunchKernelEx(&cfg, combine_kernel<4, 16, true>, meta, seqlens, q_lens, max_blocks, B, s_q, M, part_o,
-                              part_lse, o, lse, tok_rep, tok_causal, window, sinks);
-  if (by_seq)
-    return cudaLaunchKernelEx(&cfg, combine_kernel<1, 2, true>, meta, seqlens, q_lens, max_blocks, B, s_q, M, part_o,
-                              part_lse, o, lse, tok_rep, tok_causal, window, sinks);
-  return cudaLaunchKernelEx(&cfg, combine_kernel<1, 2, false>, meta, seqlens, q_lens, max_blocks, B, s_q, M, part_o,
-                            part_lse, o, lse, tok_rep, tok_causal, window, sinks);
+  const uint64_t signature = schedule_signature(B, s_q, M / s_q, P, tok_rep, tok_causal, window, sinks);
+  auto launch = [&](auto* kernel) {
+    return cudaLaunchKernelEx(&cfg, kernel, meta, seqlens, q_lens, max_blocks, B, s_q, M, signature, part_o, part_lse,
+                              o, lse, tok_rep, tok_causal, window, sinks);
+  };
+  if (wide) return launch(window > 0 ? combine_kernel<4, 16, true, true> : combine_kernel<4, 16, true, false>);
+  if (by_seq) return launch(window > 0 ? combine_kernel<1, 2, true, true> : combine_kernel<1, 2, true, false>);
+  return launch(window > 0 ? combine_kernel<1, 2, false, true> : combine_kernel<1, 2, false, false>);
 }
 
 }  // namespace mla

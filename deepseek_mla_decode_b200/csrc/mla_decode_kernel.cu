@@ -447,10 +447,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int P = p.meta[kHdrNumParts];
   int T = p.meta[kHdrNumTiles];
-  if (p.meta[kHdrMagic] != kMetaMagic || p.meta[kHdrB] != p.B || p.meta[kHdrSq] != p.s_q ||
+  if (p.meta[kHdrMagic] != (kWin ? kMetaMagicWin : kMetaMagic) || p.meta[kHdrB] != p.B || p.meta[kHdrSq] != p.s_q ||
       p.meta[kHdrH] != p.H || P * T * 2 != (int)gridDim.x || p.meta[kHdrTokens] != p.tok_rep ||
-      (p.tok_rep != 0 && p.meta[kHdrTokCausal] != p.tok_causal) || p.meta[kHdrWindow] != p.window ||
-      p.meta[kHdrSinks] != p.sinks) {
+      (p.tok_rep != 0 && p.meta[kHdrTokCausal] != p.tok_causal) ||
+      (kWin && (p.meta[kHdrWindow] != p.window || p.meta[kHdrSinks] != p.sinks))) {
     if (tid == 0 && blockIdx.x == 0) set_status(p, kErrMetadata);
     T = 0;  // every role skips; the CTA still joins the cluster barriers below
   }

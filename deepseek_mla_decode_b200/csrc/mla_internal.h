@@ -47,8 +47,23 @@ enum HdrField : int {
   kHdrTokCausal = 11, // token schedule: the causal flag the lengths were built with
   kHdrWindow = 12,    // windowed schedule: keys in the window; 0 otherwise
   kHdrSinks = 13,     // windowed schedule: first keys that stay visible
+  kHdrSignature = 14, // two words: schedule_signature of what the schedule was made for
 };
-constexpr int32_t kMetaMagic = 0x4D4C4131;  // "MLA1"
+constexpr int32_t kMetaMagic = 0x4D4C4131;     // "MLA1"
+constexpr int32_t kMetaMagicWin = 0x4D4C4157;  // "MLAW": a windowed schedule
+
+// What a schedule was made for, in one 64-bit word for the LSE combine: the attention kernel
+// checks the header's fields and runs no piece of another call's schedule, whose slots then
+// hold nothing and may lie outside the workspace.  (The combine's own check of the fields
+// made a decode of 64 sequences 1 us longer: its few registers are all in use.)
+inline uint64_t schedule_signature(int B, int s_q, int H, int P, int tok_rep, int tok_causal, int window, int sinks) {
+  uint64_t h = static_cast<uint32_t>(kMetaMagic);
+  for (int v : {B, s_q, H, P, tok_rep, tok_rep ? tok_causal : 0, window, sinks}) {
+    h = (h ^ static_cast<uint32_t>(v)) * 0x9E3779B97F4A7C15u;
+    h ^= h >> 32;
+  }
+  return h;
+}
 
 // Token schedule: the decode of B sequences with up to `rep` query tokens each (q of
 // them real) runs as an s_q = 1 decode of B * rep sequences; sequence u = b * rep + t

@@ -70,7 +70,7 @@ struct Lengths {
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) metadata_kernel(const Lengths len_of, int B,
-                                                            int s_q, int H, int num_workers,
+                                                            int s_q, int H, int num_workers, uint64_t signature,
                                                             int32_t* __restrict__ meta) {
   __shared__ int64_t scratch[32];
   __shared__ int64_t s_carry, s_total;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) metadata_kernel(const Lengths len_of
       }
     }
     if (tid == 0) {
-      meta[kHdrMagic] = kMetaMagic;
+      meta[kHdrMagic] = len_of.window > 0 ? kMetaMagicWin : kMetaMagic;
       meta[kHdrB] = B;
       meta[kHdrSq] = s_q;
       meta[kHdrH] = H;
@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kThreads) metadata_kernel(const Lengths len_of
       meta[kHdrTokCausal] = len_of.rep ? len_of.causal : 0;
       meta[kHdrWindow] = len_of.window;
       meta[kHdrSinks] = len_of.sinks;
+      *reinterpret_cast<uint64_t*>(meta + kHdrSignature) = signature;
     }
     return;
   }
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) metadata_kernel(const Lengths len_of
     }
   }
   if (tid == 0) {
-    meta[kHdrMagic] = kMetaMagic;
+    meta[kHdrMagic] = len_of.window > 0 ? kMetaMagicWin : kMetaMagic;
     meta[kHdrB] = B;
     meta[kHdrSq] = s_q;
     meta[kHdrH] = H;
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(kThreads) metadata_kernel(const Lengths len_of
     meta[kHdrTokCausal] = len_of.rep ? len_of.causal : 0;
     meta[kHdrWindow] = len_of.window;
     meta[kHdrSinks] = len_of.sinks;
+    *reinterpret_cast<uint64_t*>(meta + kHdrSignature) = signature;
   }
 }
 
@@ -274,10 +276,13 @@ cudaError_t launch_metadata(const int32_t* seqlens, int B, int s_q, int H, int n
                             int32_t* meta, cudaStream_t stream, const int32_t* q_lens, int rep, int causal,
                             int window, int sinks) {
   const Lengths len_of{seqlens, q_lens, rep, causal, window, sinks};
+  const int T = (s_q * H + kRowsPerTile - 1) / kRowsPerTile;
+  const uint64_t sig =
+      schedule_signature(B, s_q, H, num_workers < T ? 1 : num_workers / T, rep, causal, window, sinks);
   if (B <= 256)
-    metadata_kernel<256><<<1, 256, 0, stream>>>(len_of, B, s_q, H, num_workers, meta);
+    metadata_kernel<256><<<1, 256, 0, stream>>>(len_of, B, s_q, H, num_workers, sig, meta);
   else
-    metadata_kernel<1024><<<1, 1024, 0, stream>>>(len_of, B, s_q, H, num_workers, meta);
+    metadata_kernel<1024><<<1, 1024, 0, stream>>>(len_of, B, s_q, H, num_workers, sig, meta);
   return cudaGetLastError();
 }
 

@@ -360,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int P = p.meta[kHdrNumParts];
-  const bool bad_meta = p.meta[kHdrMagic] != kMetaMagic || p.meta[kHdrB] != p.B || p.meta[kHdrSq] != 1 ||
+  const bool bad_meta = p.meta[kHdrMagic] != kMetaMagicWin || p.meta[kHdrB] != p.B || p.meta[kHdrSq] != 1 ||
                         p.meta[kHdrH] != p.M || p.meta[kHdrNumTiles] != 1 || P * 2 != (int)gridDim.x ||
                         p.meta[kHdrTokens] != p.rep || p.meta[kHdrTokCausal] != 1 ||
                         p.meta[kHdrWindow] != p.window || p.meta[kHdrSinks] != p.sinks;

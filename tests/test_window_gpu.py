@@ -401,3 +401,24 @@ def test_window_with_the_callers_buffers_and_stream_argument():
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
     assert torch.equal(out2, want) and torch.equal(lse2, want_lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens", [[9000, 7000], [900 + 37 * i for i in range(100)]], ids=["wide", "by_partition"])
+def test_split_sequences_of_another_schedule_are_left(lens, fp8):
+    """Sequences in several pieces: the merge must not touch them either."""
+    p = Problem(lens, 1, 128, 8000, 4, seed=31)
+    n = i32(p.lens)
+    kv = torch.from_numpy(p.packed()).cuda() if fp8 else dev(p.kv)
+    args = dev(p.q_nope), dev(p.q_pe), kv, i32(p.table), n, None, SCALE_192
+    call = mla.decode_fp8_window if fp8 else mla.decode_window
+    B = len(lens)
+    splits = mla.get_metadata_window(n, None, 1, 128, 8000, 4).cpu().numpy()[16 + 4 * 256 + 2 * B:][:B]
+    assert splits.max() > 1
+    for meta in (mla.get_metadata_window(n, None, 1, 128, 8001, 4), mla.get_metadata_window(n, None, 1, 128, 8000, 5)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full((B, 1, 128, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((B, 1, 128), 7.0, device="cuda")
+        call(*args, 8000, 4, meta, out=out, lse=lse, status=status)
+        assert int(status.item()) == mla.MLA_DEVICE_ERR_METADATA
+        assert (out == 7).all() and (lse == 7).all()
