@@ -511,9 +511,9 @@ def _device_index(t):
 
 
 def _new(like, stream, shape, dtype=None):
-    """An uninitialised tensor (None: of like's dtype) for a launch on `stream`.  It comes from that stream's memory
-    pool: memory of the current stream's pool may still be in use there, and a workspace goes
-    back to its pool before the kernels that use it have run."""
+    """An uninitialised tensor (None: of like's dtype) for a launch on `stream`.  It comes
+    from that stream's memory pool: memory of the current stream's pool may still be in use
+    there, and a workspace goes back to its pool before the kernels that use it have run."""
     if stream is None:
         return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
     with _torch.cuda.stream(stream):

@@ -25,10 +25,11 @@ cudaError_t decode_kernel_setup(int device);
 cudaError_t window_fp8_setup();
 cudaError_t launch_window_fp8(const CUtensorMap& tm_rows, const CUtensorMap& tm_qn, const CUtensorMap& tm_qp,
                               const CUtensorMap& tm_out, const CUtensorMap& tm_part, const void* rows,
-                              const int32_t* block_table, int max_blocks, const int32_t* seqlens, const int32_t* q_lens, const int32_t* meta,
-                              int64_t num_blocks, int units, int rep, int H, float scale, int window, int sinks,
-                              void* out, float* lse, float* part_lse, int32_t* status, int num_ctas,
-                              uint64_t wait_timeout_ns, int inject_stall, cudaStream_t stream);
+                              const int32_t* block_table, int max_blocks, const int32_t* seqlens,
+                              const int32_t* q_lens, const int32_t* meta, int64_t num_blocks, int units, int rep,
+                              int H, float scale, int window, int sinks, void* out, float* lse, float* part_lse,
+                              int32_t* status, int num_ctas, uint64_t wait_timeout_ns, int inject_stall,
+                              cudaStream_t stream);
 namespace sage {
 cudaError_t attention_setup();
 cudaError_t launch_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,

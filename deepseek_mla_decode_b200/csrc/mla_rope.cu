@@ -39,8 +39,8 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 template <bool kHalf, bool kSplit, bool kSkipPadding>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32) rope_q_kernel(
     const __nv_bfloat16* q, int64_t row_stride, const int32_t* seqlens, const int32_t* q_lens, uint32_t rows,
-    const __grid_constant__ RowDiv per_seq, int H, const __grid_constant__ RopeTurns rope, __nv_bfloat16* q_heads, __nv_bfloat16* q_pe,
-    int32_t* status) {
+    const __grid_constant__ RowDiv per_seq, int H, const __grid_constant__ RopeTurns rope, __nv_bfloat16* q_heads,
+    __nv_bfloat16* q_pe, int32_t* status) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;

@@ -23,8 +23,8 @@
 // and dims 256h + 128r + (0..127) as its half of the PV operand.  One box of the cache, 64
 // rows x 128 code bytes, serves both: K-major for QK, MN-major for PV.
 //
-// Measured (192 sequences, 128 heads, window 4096, attention and combine): 264-271 us on the
-// pool's boxes, 49 % of the tensor floor, against 432 us for the kernel that converts codes to
+// Measured (192 sequences, 128 heads, window 4096, attention and combine): 261-270 us,
+// 49 % of the tensor floor, against 432 us for the kernel that converts codes to
 // bf16.  No unit is busy half the time (tensor pipe 45 %, issue 39 %, DRAM 28 %); a tile of
 // 9.7 k cycles is the softmax's two passes (5 k), its hand-offs (3 k) and, spread over 13
 // tiles, the switch of pieces (0.9 k: the new query's terms and the old output).  The
@@ -1160,10 +1160,11 @@ cudaError_t window_fp8_setup() {
 
 cudaError_t launch_window_fp8(const CUtensorMap& tm_rows, const CUtensorMap& tm_qn, const CUtensorMap& tm_qp,
                               const CUtensorMap& tm_out, const CUtensorMap& tm_part, const void* rows,
-                              const int32_t* block_table, int max_blocks, const int32_t* seqlens, const int32_t* q_lens, const int32_t* meta,
-                              int64_t num_blocks, int units, int rep, int H, float scale, int window, int sinks,
-                              void* out, float* lse, float* part_lse, int32_t* status, int num_ctas,
-                              uint64_t wait_timeout_ns, int inject_stall, cudaStream_t stream) {
+                              const int32_t* block_table, int max_blocks, const int32_t* seqlens,
+                              const int32_t* q_lens, const int32_t* meta, int64_t num_blocks, int units, int rep,
+                              int H, float scale, int window, int sinks, void* out, float* lse, float* part_lse,
+                              int32_t* status, int num_ctas, uint64_t wait_timeout_ns, int inject_stall,
+                              cudaStream_t stream) {
   Params prm;
   std::memset(&prm, 0, sizeof(prm));
   prm.tm_rows = tm_rows;

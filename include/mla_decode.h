@@ -244,8 +244,9 @@ mla_status_t mla_decode_fp8_window(const void* q_nope, const void* q_pe, const v
  *   it separately is a library convenience (timing, custom merges).
  * mla_decode_combine: the LSE-combine kernel (split-K merge, "DeepSeek speed test /
  *   FA3" article section 2.1): for every split sequence, lse = ln sum_s exp(lse_s) and
- *   out = sum_s exp(lse_s - lse) O_s.  Only split sequences are touched; `status` is
- *   accepted for symmetry and never written.
+ *   out = sum_s exp(lse_s - lse) O_s.  Only split sequences are touched, and none
+ *   with a schedule made for other arguments; `status` is accepted for symmetry and never
+ *   written.
  */
 mla_status_t mla_decode_attention(const void* q_nope, const void* q_pe, const void* kv_cache,
                                   int64_t num_blocks, const int32_t* block_table, int max_blocks,
