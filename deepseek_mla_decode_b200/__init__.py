@@ -567,6 +567,12 @@ def _window_sizes(index, units, H):
     return metadata_size(units, 1, H), workspace_size(units, 1, H)
 
 
+def _window_range(window, sinks):
+    """Refuses what a C int would cut to another number (the library judges the rest)."""
+    if window > 0x7FFFFFFF or sinks > 0x7FFFFFFF:
+        raise ValueError("window and sinks must be below 2^31")
+
+
 def rope_q(q, cache_seqlens, rope: Rope, q_lens=None, q_heads=None, q_pe=None, status=None, stream=None):
     """mla_rope_q: splits query heads q [B, s_q, H, 192] = [128 | 64 rotary] into q_heads
     [B, s_q, H, 128] (for absorb_q) and q_pe [B, s_q, H, 64] (for decode), the latter rotated
@@ -665,6 +671,7 @@ def get_metadata_window(cache_seqlens, q_lens, s_q: int, H: int, window: int, si
     """mla_get_metadata_window: the schedule for decode_window / decode_fp8_window (shared by
     every layer of a step); q_lens may be None."""
     i32 = (_torch or _torch_module()).int32
+    _window_range(window, sinks)
     (B,) = cache_seqlens.shape
     index = _device_index(cache_seqlens)
     handle = _launch_stream(index, stream)
@@ -683,6 +690,7 @@ def get_metadata_window(cache_seqlens, q_lens, s_q: int, H: int, window: int, si
 def _decode_window(fn, q_nope, q_pe, kv, width, dtype, block_table, cache_seqlens, q_lens, softmax_scale, window, sinks,
                    metadata, workspace, out, lse, status, stream):
     bf16, f32, i32 = _torch.bfloat16, _torch.float32, _torch.int32
+    _window_range(window, sinks)
     shape, pool, table = q_nope.shape, kv.shape, block_table.shape
     if len(shape) != 4 or len(pool) != 3 or len(table) != 2:
         raise ValueError("q_nope [B, s_q, H, 512], cache [num_blocks, 64, width], block_table [B, max_blocks] expected")

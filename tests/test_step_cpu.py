@@ -206,3 +206,17 @@ def test_window_metadata_refusals(code, kw):
     a = dict(n=P, q_lens=None, B=2, s_q=2, H=16, window=64, sinks=4, meta=P, meta_bytes=1 << 20, stream=None)
     a.update(kw)
     assert mla.load_library().mla_get_metadata_window(*a.values()) == code
+
+
+@pytest.mark.parametrize("window,sinks", [(2**32 + 100, 4), (2**31, 0), (100, 2**32), (100, 2**31)])
+def test_window_sizes_beyond_an_int_are_refused(window, sinks):
+    """A C int would cut them: 2^32 + 100 keys to 100."""
+    torch = pytest.importorskip("torch")
+    n = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="2\\^31"):
+        mla.get_metadata_window(n, None, 1, 16, window, sinks)
+    q = torch.zeros(2, 1, 16, 512, dtype=torch.bfloat16)
+    for call, cache in ((mla.decode_window, torch.zeros(1, 64, 576, dtype=torch.bfloat16)),
+                        (mla.decode_fp8_window, torch.zeros(1, 64, 656, dtype=torch.uint8))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call(q, q[..., :64].contiguous(), cache, torch.zeros(2, 1, dtype=torch.int32), n, None, 0.1, window, sinks, n)
