@@ -3,16 +3,23 @@
 // Math: mla_decode_kernel.cu's, over the token schedule and a window's visible blocks
 // (window_blocks).  A cache row is s * [code | k'], code e4m3 (512), k' bf16 (64), s fp32.
 //
-// Both products are e4m3 x e4m3 (tcgen05 kind::f8f6f4, fp32 accumulators), and the operand
-// that is not a code goes in as two e4m3 terms, the rounded value and what rounding left:
-//   QK:  q * 2^j = q_hi + q_lo, the power of two taking the row's largest value to
+// Both products are of 8-bit floats (tcgen05 kind::f8f6f4, fp32 accumulators), and the operand
+// that is not a code goes in as two terms, the rounded value and what rounding left:
+//   QK:  q * 2^j = q_hi + q_lo in e4m3, the power of two taking the row's largest value to
 //        [128, 256).  A bf16 value's 8 bits are 4 + 4 bits, so the split is exact down to
-//        2^-2 (2^-10 of the row's maximum) and off by at most 2^-10 below that.  k' splits
+//        2^-2 (2^-10 of the row's maximum) and off by at most 1.5 * 2^-10 below that.  k' splits
 //        the same way into [k'_hi | k'_lo], a fifth 128-wide chunk beside the four of codes,
 //        against [q_hi | q_hi] and [q_lo | q_lo].
-//   PV:  P = 2^(x - m) * s = P_hi + P_lo, m the running maximum of x + log2 s, lazily: P stays
-//        in [0, 2^8.6] and the terms' smallest step is 2^-14 of the largest weight s 2^x or
-//        finer, whatever the scales are.  The normaliser l = sum 2^(x - m) is fp32.
+//   PV:  P = 2^(x - m) * s = P_hi + P_lo, P_hi in e4m3 and P_lo, what its code left of P (its
+//        smallest steps included), in e5m2, whose range carries on where e4m3's ends: off by at
+//        most 2^-8 of P down to 2^-6, 2^-14 below that, 2^-17 and less below 2^-14.  Every key
+//        counts: where one key takes most of the weight (the first keys, which are kept visible
+//        for that), thousands share the rest, and a grid fixed by the largest loses them.  So m
+//        follows the largest x + log2 s of each tile, up and down, lazily: a tile's largest P
+//        stays in [2^2, 2^8.5), O is rescaled when it would leave that, and a weight is off by
+//        at most 2^-8 of itself or 2^-16 of its tile's largest (a tile's 256 keys together lose
+//        less than 2^-8 of that one).  The normaliser l = sum 2^(x - m) is fp32, in the unit of
+//        the row's largest.
 // Two 8-bit MMAs take the time of one bf16 MMA, so this costs no tensor time over the bf16
 // cache, moves half its bytes through the ring, and converts nothing but the 64 rotary
 // values a key.
@@ -76,17 +83,22 @@ static_assert(4 * kEpiRoundBytes <= kSmemRot, "the last epilogue's staging stays
 constexpr int kRegsIssue = 88, kRegsPrep = 88, kRegsSoftmax = 168;
 static_assert(128 * (kRegsIssue + kRegsPrep) + 256 * kRegsSoftmax == kThreads * 128, "register split");
 constexpr uint32_t kTmemO = 0, kTmemS0 = 256, kTmemCols = 512;
-// P <= 2^(kHeadroom + kRescaleThreshold + 0.086) < 2^8.6 < 448.  More headroom makes small
-// weights finer, a larger threshold rescales O less often.
-constexpr float kHeadroom = 5.0f, kRescaleThreshold = 3.5f;
-constexpr float kLogUnit = 0x1p15f;
-constexpr float kBias = kHeadroom + 383.0f;  // the logarithm read off the bits is 383 high
+// The largest P of a tile is 2^kHeadroom where a unit is taken and stays in
+// [2^(kHeadroom - kFall), 2^(kHeadroom + kRise)) = [2^2, 2^8.5) while it is kept: below e4m3's
+// 448, and high enough for e5m2's smallest steps.  Units taken at 2^5 to 2^7.5 within these
+// bounds cost the same (262.0 to 262.8 us, 192 sequences); higher ones are finer, but O is
+// rescaled sooner where scores grow along the window.
+constexpr float kHeadroom = 6.0f, kRise = 2.5f, kFall = 4.0f;
+// The unit falls at most this far below the row's largest: what a tile below that adds is not
+// worth its exponent (2^-40 a key), and O stays far from fp32's range.
+constexpr float kUnitFloor = 40.0f;
 // Scales below this count as it: a row of zeros (scale 0) still weighs 2^x in the
 // normaliser, and 2^x is kept in units of the largest x + log2 s.
 constexpr float kMinScale = 0x1p-100f;
 constexpr int kMaxUp = 100;  // largest power of two of a query row
 constexpr uint32_t kIdescQK = make_idesc_e4m3(128, 256, false, false);
 constexpr uint32_t kIdescPV = make_idesc_e4m3(128, 256, false, true);
+constexpr uint32_t kIdescPVLo = kIdescPV | kIdescAE5M2;  // P_lo
 constexpr int kBarSoftmax = 1, kBarPrep = 2;
 constexpr uint64_t kDrainWaitNs = 100000000ull;  // bound on the post-abort wait for tensor-core work
 constexpr uint64_t kQuiesceNs = 500000ull;       // post-abort wait for TMA loads in flight
@@ -264,6 +276,27 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
   const float ta = top4(a), tb = top4(b), tc = top4(c), td = top4(d);
   hi = e4m3x4(ta, tb, tc, td);
   lo = e4m3x4(a - ta, b - tb, c - tc, d - td);
+}
+// Four weights as two terms each: hi the weight rounded to e4m3, lo what hi left, read back off
+// the codes, rounded to e5m2.
+__device__ __forceinline__ void split2(float a, float b, uint16_t& hi, uint16_t& lo) {
+  asm("{\n\t.reg .b32 h;\n\t.reg .b16 x, y, m;\n\t.reg .f32 p, q;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 %0, %3, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 h, %0;\n\t"
+      "mov.b32 {x, y}, h;\n\t"
+      "mov.b16 m, 0xBC00;\n\t"  // -1
+      "fma.rn.f32.f16 p, x, m, %2;\n\t"
+      "fma.rn.f32.f16 q, y, m, %3;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 %1, q, p;\n\t}"
+      : "=&h"(hi), "=&h"(lo)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void split_weights(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
+  uint16_t h0, l0, h1, l1;
+  split2(a, b, h0, l0);
+  split2(c, d, h1, l1);
+  hi = h0 | ((uint32_t)h1 << 16);
+  lo = l0 | ((uint32_t)l1 << 16);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -562,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int ks = 0; ks < 2; ++ks) {
                 const bool on = elected && ks >= ks0 && ks < ks1;
                 umma8_2sm_if(on, tmem + kTmemO + 128 * h, a0 + 2 * ks, b0 + 256 * ks, kIdescPV, !(first && ks == ks0));
-                umma8_2sm_if(on, tmem + kTmemO + 128 * h, a0 + 2 * kBoxD + 2 * ks, b0 + 256 * ks, kIdescPV, 1);
+                umma8_2sm_if(on, tmem + kTmemO + 128 * h, a0 + 2 * kBoxD + 2 * ks, b0 + 256 * ks, kIdescPVLo, 1);
               }
             }
             commit_2sm_if(elected, smem_u32(&ctrl.empty[slot]));
@@ -700,7 +733,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       while (go && walk.next(pc)) {
         const int nt = num_tiles(pc);
-        float m_used = -INFINITY, l_part = 0.f, rs = 0.f;
+        // m_used: the unit of P and O, m_l: that of l, the largest m_used so far
+        float m_used = -INFINITY, m_l = -INFINITY, l_part = 0.f, rs = 0.f;
         const int nsplit = p.meta[off_num_splits(p.B) + pc.b];
         const int split_base = p.meta[off_split_prefix(p.B) + pc.b];
         int bad_ids = 0;
@@ -729,8 +763,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           auto seen = [&](int c) -> bool { return (uint32_t)(c - c0) < (uint32_t)cnt; };
           const bool full = __all_sync(0xffffffffu, cnt == kBlockSize);
           // x = S * s * rs with the key's scale s and rs = 2^-j * scale * log2 e; the maximum is
-          // of z = x + log2 s.  The table holds s and lg = 2^15 (log2 s + 383), the logarithm
-          // read off s's bits (at most 0.087 low); z is kept in lg's units.
+          // of z = x + log2 s.  The table holds s and log2 s.
           const float4* tab = reinterpret_cast<const float4*>(smem + kSmemTab + buf * kTabBytes) + 16 * (2 * hk + g);
           // hidden keys of a group that starts at key c score -inf: their weight is 2^-inf = 0
           auto hide = [&](uint32_t* s, int c, int count) {
@@ -742,7 +775,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           };
           auto score = [](uint32_t s) -> float { return __uint_as_float(s); };
           float mx0 = -INFINITY, mx1 = -INFINITY;
-          const uint64_t rsz = pack_f32x2(rs * kLogUnit, rs * kLogUnit);
+          const uint64_t rs2 = pack_f32x2(rs, rs);
 #pragma unroll 1
           for (int c = 0; c < 64; c += 16) {
             uint32_t s[16];
@@ -754,8 +787,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const uint64_t y01 = mul2(pack_f32x2(score(s[i]), score(s[i + 1])), pack_f32x2(f.x, f.y));
               const uint64_t y23 = mul2(pack_f32x2(score(s[i + 2]), score(s[i + 3])), pack_f32x2(f.z, f.w));
               float z0, z1, z2, z3;
-              unpack_f32x2(fma2(y01, rsz, pack_f32x2(lg.x, lg.y)), z0, z1);
-              unpack_f32x2(fma2(y23, rsz, pack_f32x2(lg.z, lg.w)), z2, z3);
+              unpack_f32x2(fma2(y01, rs2, pack_f32x2(lg.x, lg.y)), z0, z1);
+              unpack_f32x2(fma2(y23, rs2, pack_f32x2(lg.z, lg.w)), z2, z3);
               mx0 = max3(mx0, z0, z1);
               mx1 = max3(mx1, z2, z3);
             }
@@ -763,20 +796,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ctrl.red_max[buf][2 * hk + g][m] = fmaxf(mx0, mx1);
           go = named_bar_and(kBarSoftmax, kNumSoftmaxThreads, ok);
           if (!go) break;
-          const float m_new =
-              fmaxf(fmaxf(m_used, fmaxf(ctrl.red_max[buf][0][m], ctrl.red_max[buf][1][m])),
-                    fmaxf(ctrl.red_max[buf][2][m], ctrl.red_max[buf][3][m]));
-          const bool rescale = m_new > m_used + kRescaleThreshold * kLogUnit;
+          const float top = fmaxf(fmaxf(ctrl.red_max[buf][0][m], ctrl.red_max[buf][1][m]),
+                                  fmaxf(ctrl.red_max[buf][2][m], ctrl.red_max[buf][3][m]));
+          // the unit this tile's largest weight asks for
+          const float want = fmaxf(top, m_l - kUnitFloor);
+          const bool rescale = want > m_used + kRise || want < m_used - kFall;
           float alpha = 1.f;
           if (rescale) {
-            alpha = (m_used == -INFINITY) ? 0.f : fast_exp2((m_used - m_new) * (1.0f / kLogUnit));
-            m_used = m_new;
-            l_part *= alpha;
+            alpha = (m_used == -INFINITY) ? 0.f : fast_exp2(m_used - want);
+            m_used = want;
+            if (m_used > m_l) {
+              l_part *= (m_l == -INFINITY) ? 0.f : fast_exp2(m_l - m_used);
+              m_l = m_used;
+            }
           }
-          const float nref = (m_used == -INFINITY) ? 0.f : kBias - m_used * (1.0f / kLogUnit);
+          const float beta = (m_used == m_l) ? 1.f : fast_exp2(m_used - m_l);
+          const float nref = (m_used == -INFINITY) ? 0.f : kHeadroom - m_used;
           // weights: P of keys 0..31 in pa, of 32..63 in pb (8 words of hi, 8 of lo terms)
           uint64_t l01 = pack_f32x2(0.f, 0.f), l23 = l01;
-          const uint64_t rs2 = pack_f32x2(rs, rs), nref2 = pack_f32x2(nref, nref);
+          const uint64_t nref2 = pack_f32x2(nref, nref);
           uint32_t pa[16], pb[16] = {};
 #pragma unroll 1
           for (int c = 0; c < 64; c += 32) {
@@ -798,13 +836,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               l23 = add2(l23, e23);
               unpack_f32x2(mul2(e01, f01), e0, e1);
               unpack_f32x2(mul2(e23, f23), e2, e3);
-              split4(e0, e1, e2, e3, pb[q], pb[8 + q]);
+              split_weights(e0, e1, e2, e3, pb[q], pb[8 + q]);
             }
           }
           {
             float l0, l1;
             unpack_f32x2(add2(l01, l23), l0, l1);
-            l_part += l0 + l1;
+            l_part = fmaf(beta, l0 + l1, l_part);
           }
           // PV of the previous tile (possibly the previous piece's last) must be done before
           // P is overwritten, O is rescaled or the previous piece's O is read
@@ -892,8 +930,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool bad = ctrl.bad_piece != 0;
         const float nanf_ = __int_as_float(0x7fc00000);
         // NaN scales make the row NaN; so does a NaN among the visible scores (l is NaN then)
-        pend_sc = (bad || l_row != l_row) ? nanf_ : ((l_row > 0.f) ? 1.f / l_row : 0.f);
-        const float lse2 = m_used * (1.0f / kLogUnit) - kBias + __log2f(l_row);
+        const float unit = (m_used == m_l) ? 1.f : fast_exp2(m_used - m_l);  // O's in l's
+        pend_sc = (bad || l_row != l_row) ? nanf_ : ((l_row > 0.f) ? unit / l_row : 0.f);
+        const float lse2 = m_l - kHeadroom + __log2f(l_row);
         pend_lse = (bad || l_row != l_row) ? nanf_ : ((l_row > 0.f) ? lse2 * 0.69314718055994531f : -INFINITY);
         pend_direct = (nsplit == 1);
         pend_b = pc.b;
@@ -1030,7 +1069,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float f = seen ? s : 1.0f;         // a hidden key's scale may be anything
         if (f < kMinScale) f = kMinScale;  // a NaN stays one
         tab[key] = f;
-        tab[kTileKeys + key] = (float)(__float_as_int(f) >> 8) + 0x1p23f;
+        tab[kTileKeys + key] = __log2f(f);
       };
       auto split_rotary = [&]() {
         const int j = lane & 7;

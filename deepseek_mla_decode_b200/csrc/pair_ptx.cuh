@@ -18,7 +18,7 @@ __device__ __forceinline__ void umma_2sm_if(bool on, uint32_t d, uint64_t a, uin
       "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)on)
       : "memory");
 }
-// kind::f8f6f4: 8-bit floats (e4m3 in both operands here), 32 of them a step of K
+// kind::f8f6f4: 8-bit floats (e4m3, or e5m2 as idesc says), 32 of them a step of K
 __device__ __forceinline__ void umma8_2sm_if(bool on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                              uint32_t acc) {
   asm volatile(

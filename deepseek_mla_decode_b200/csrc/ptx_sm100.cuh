@@ -216,7 +216,9 @@ __host__ __device__ constexpr uint32_t make_idesc_bf16(int M, int N, bool a_mn_m
          ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
-// The same for kind::f8f6f4 with e4m3 A/B (format 0) and fp32 D.
+// The same for kind::f8f6f4 with e4m3 A/B (format 0) and fp32 D; the operands' formats are
+// independent of each other, and the bit below makes A e5m2 (format 1).
+constexpr uint32_t kIdescAE5M2 = 1u << 7;
 __host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
