@@ -4,22 +4,21 @@
 // (window_blocks).  A cache row is s * [code | k'], code e4m3 (512), k' bf16 (64), s fp32.
 //
 // Both products are of 8-bit floats (tcgen05 kind::f8f6f4, fp32 accumulators), and the operand
-// that is not a code goes in as two terms, the rounded value and what rounding left:
-//   QK:  q * 2^j = q_hi + q_lo in e4m3, the power of two taking the row's largest value to
-//        [128, 256).  A bf16 value's 8 bits are 4 + 4 bits, so the split is exact down to
-//        2^-2 (2^-10 of the row's maximum) and off by at most 1.5 * 2^-10 below that.  k' splits
-//        the same way into [k'_hi | k'_lo], a fifth 128-wide chunk beside the four of codes,
-//        against [q_hi | q_hi] and [q_lo | q_lo].
-//   PV:  P = 2^(x - m) * s = P_hi + P_lo, P_hi in e4m3 and P_lo, what its code left of P (its
-//        smallest steps included), in e5m2, whose range carries on where e4m3's ends: off by at
-//        most 2^-8 of P down to 2^-6, 2^-14 below that, 2^-17 and less below 2^-14.  Every key
-//        counts: where one key takes most of the weight (the first keys, which are kept visible
-//        for that), thousands share the rest, and a grid fixed by the largest loses them.  So m
-//        follows the largest x + log2 s of each tile, up and down, lazily: a tile's largest P
-//        stays in [2^2, 2^8.5), O is rescaled when it would leave that, and a weight is off by
-//        at most 2^-8 of itself or 2^-16 of its tile's largest (a tile's 256 keys together lose
-//        less than 2^-8 of that one).  The normaliser l = sum 2^(x - m) is fp32, in the unit of
-//        the row's largest.
+// that is not a code goes in as two terms: hi, the value rounded to e4m3, and lo, what hi's code
+// left of it (its smallest steps included) rounded to e5m2.  Four bits, three and lo's sign are
+// the eight of a bf16 value, and e5m2's range carries on where e4m3's ends: off by at most
+// 2^-8 of the value down to 2^-6, 2^-14 below that, 2^-17 and less below 2^-14.
+//   QK:  q * 2^j = q_hi + q_lo, the power of two taking the row's largest value to
+//        [128, 256): exact down to 2^-6, 2^-13 of the row's largest.  k' splits the same way
+//        into [k'_hi | k'_lo], a fifth 128-wide chunk beside the four of codes, against
+//        [q_hi | q_hi] and [q_lo | q_lo].
+//   PV:  P = 2^(x - m) * s = P_hi + P_lo.  Every key counts: where one key takes most of the
+//        weight (the first keys, which are kept visible for that), thousands share the rest, and
+//        a grid fixed by the largest loses them.  So m follows the largest x + log2 s of each
+//        tile, up and down, lazily: a tile's largest P stays in [2^2, 2^8.5), O is rescaled
+//        when it would leave that, and a weight is off by at most 2^-8 of itself or 2^-16 of
+//        its tile's largest (a tile's 256 keys together lose less than 2^-8 of that one).  The
+//        normaliser l = sum 2^(x - m) is fp32, in the unit of the row's largest.
 // Two 8-bit MMAs take the time of one bf16 MMA, so this costs no tensor time over the bf16
 // cache, moves half its bytes through the ring, and converts nothing but the 64 rotary
 // values a key.
@@ -98,7 +97,7 @@ constexpr float kMinScale = 0x1p-100f;
 constexpr int kMaxUp = 100;  // largest power of two of a query row
 constexpr uint32_t kIdescQK = make_idesc_e4m3(128, 256, false, false);
 constexpr uint32_t kIdescPV = make_idesc_e4m3(128, 256, false, true);
-constexpr uint32_t kIdescPVLo = kIdescPV | kIdescAE5M2;  // P_lo
+constexpr uint32_t kLoA = kIdescAE5M2, kLoB = kIdescBE5M2;  // the operand is of low terms
 constexpr int kBarSoftmax = 1, kBarPrep = 2;
 constexpr uint64_t kDrainWaitNs = 100000000ull;  // bound on the post-abort wait for tensor-core work
 constexpr uint64_t kQuiesceNs = 500000ull;       // post-abort wait for TMA loads in flight
@@ -257,27 +256,7 @@ __device__ __forceinline__ bool wait_bar(Ctrl* c, const Params& p, uint32_t bar,
   }
 }
 
-// Four values as two e4m3 terms each: hi the value rounded to e4m3's four bits (an fp32 add
-// and mask: ties away, above the smallest normal), lo what that left.
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 x, y;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\t"
-      "mov.b32 %0, {x, y};\n\t}"
-      : "=r"(r)
-      : "f"(a), "f"(b), "f"(c), "f"(d));
-  return r;
-}
-__device__ __forceinline__ float top4(float x) {
-  return __int_as_float((__float_as_int(x) + 0x80000) & 0xfff00000);
-}
-__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
-  const float ta = top4(a), tb = top4(b), tc = top4(c), td = top4(d);
-  hi = e4m3x4(ta, tb, tc, td);
-  lo = e4m3x4(a - ta, b - tb, c - tc, d - td);
-}
-// Four weights as two terms each: hi the weight rounded to e4m3, lo what hi left, read back off
+// Four values as two terms each: hi the value rounded to e4m3, lo what hi left, read back off
 // the codes, rounded to e5m2.
 __device__ __forceinline__ void split2(float a, float b, uint16_t& hi, uint16_t& lo) {
   asm("{\n\t.reg .b32 h;\n\t.reg .b16 x, y, m;\n\t.reg .f32 p, q;\n\t"
@@ -291,7 +270,7 @@ __device__ __forceinline__ void split2(float a, float b, uint16_t& hi, uint16_t&
       : "=&h"(hi), "=&h"(lo)
       : "f"(a), "f"(b));
 }
-__device__ __forceinline__ void split_weights(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
   uint16_t h0, l0, h1, l1;
   split2(a, b, h0, l0);
   split2(c, d, h1, l1);
@@ -545,8 +524,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t a0 = dq0 + 2 * c * kBoxD;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-          umma8_2sm_if(elected, d, a0 + 2 * ks, b0 + 2 * ks, kIdescQK, (c | ks) != 0);
-          umma8_2sm_if(elected, d, a0 + kBoxD + 2 * ks, b0 + 2 * ks, kIdescQK, 1);
+          const uint32_t b = (c == kCodeChunks && ks >= 2) ? kLoB : 0u;
+          umma8_2sm_if(elected, d, a0 + 2 * ks, b0 + 2 * ks, kIdescQK | b, (c | ks) != 0);
+          umma8_2sm_if(elected, d, a0 + kBoxD + 2 * ks, b0 + 2 * ks, kIdescQK | kLoA | b, 1);
         }
       };
       auto mma_qk = [&](int nt, int t) {
@@ -595,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int ks = 0; ks < 2; ++ks) {
                 const bool on = elected && ks >= ks0 && ks < ks1;
                 umma8_2sm_if(on, tmem + kTmemO + 128 * h, a0 + 2 * ks, b0 + 256 * ks, kIdescPV, !(first && ks == ks0));
-                umma8_2sm_if(on, tmem + kTmemO + 128 * h, a0 + 2 * kBoxD + 2 * ks, b0 + 256 * ks, kIdescPVLo, 1);
+                umma8_2sm_if(on, tmem + kTmemO + 128 * h, a0 + 2 * kBoxD + 2 * ks, b0 + 256 * ks, kIdescPV | kLoA, 1);
               }
             }
             commit_2sm_if(elected, smem_u32(&ctrl.empty[slot]));
@@ -836,7 +816,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               l23 = add2(l23, e23);
               unpack_f32x2(mul2(e01, f01), e0, e1);
               unpack_f32x2(mul2(e23, f23), e2, e3);
-              split_weights(e0, e1, e2, e3, pb[q], pb[8 + q]);
+              split4(e0, e1, e2, e3, pb[q], pb[8 + q]);
             }
           }
           {

@@ -217,8 +217,8 @@ __host__ __device__ constexpr uint32_t make_idesc_bf16(int M, int N, bool a_mn_m
 }
 
 // The same for kind::f8f6f4 with e4m3 A/B (format 0) and fp32 D; the operands' formats are
-// independent of each other, and the bit below makes A e5m2 (format 1).
-constexpr uint32_t kIdescAE5M2 = 1u << 7;
+// independent of each other, and the two bits below make one e5m2 (format 1).
+constexpr uint32_t kIdescAE5M2 = 1u << 7, kIdescBE5M2 = 1u << 10;
 __host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);

@@ -193,3 +193,31 @@ def test_units_that_fall_and_rise():
     p.check(whole_batch(), 2048, 40)
     p = OneKeyAhead(2048 + 40, 1300, spread=14.0, seed=9)
     p.check(whole_batch(), 2048, 40)
+
+
+# ---- query and rotary terms ------------------------------------------------------------
+@pytest.mark.parametrize("outlier", [2.0 ** 10, 2.0 ** 11])
+def test_a_query_channel_far_above_the_others(outlier):
+    """A channel that meets only zeros in the cache sets the power of two of a query row and adds
+    nothing; the others are 2^-10 and 2^-11 of it, 2^-3 and 2^-4 in units where it is 2^7.  The
+    terms of a bf16 value are exact from 2^-6 up and off by at most 2^-14 below, 2^-21 of the
+    outlier: 2^-10 at most here, on the smaller values of a row.  A score of 575 such products is
+    then off by SCALE_192 sqrt(575) 2^-10 / sqrt(3) = 1e-3 at most (one standard deviation), and
+    the lse, a weighted mean of a few dozen keys' errors, by 2e-4: inside the usual bars, which
+    terms with steps of 2^-9 in these units miss by a factor of ten."""
+    n, B, H = 700, 4, 16
+    rng = np.random.default_rng(int(np.log2(outlier)))
+    rows = rng.standard_normal((11 * 64, 576), dtype=np.float32)
+    rows[:, 7] = 0
+    packed = F.pack_cache(f32_to_bf16_bits(rows).reshape(11, 64, 576))
+    store = F.dequantize_cache(packed).reshape(-1, 576)
+    q = rng.standard_normal((B, 1, H, 576), dtype=np.float32)
+    q[..., 7] = outlier
+    qn, qp = f32_to_bf16_bits(q[..., :512]), f32_to_bf16_bits(q[..., 512:])
+    nt = i32([n] * B)
+    meta = mla.get_metadata_window(nt, None, 1, H, 512, 100)
+    out, lse = mla.decode_fp8_window(dev(qn), dev(qp), torch.from_numpy(packed).cuda(),
+                                     i32(np.tile(np.arange(11), (B, 1))), nt, None, SCALE_192, 512, 100, meta)
+    ref, ref_lse = S.window_decode_ref(O.bf16_to_f64(qn), O.bf16_to_f64(qp), lambda b, t: store[t], [n] * B, None,
+                                       SCALE_192, 512, 100)
+    compare(out.float().cpu().double().numpy(), lse.cpu().double().numpy(), ref, ref_lse, what=f"outlier {outlier}")
