@@ -567,10 +567,11 @@ def _window_sizes(index, units, H):
     return metadata_size(units, 1, H), workspace_size(units, 1, H)
 
 
-def _window_range(window, sinks):
+def _window_range(window, sinks, s_q=1, H=1):
     """Refuses what a C int would cut to another number (the library judges the rest)."""
-    if window > 0x7FFFFFFF or sinks > 0x7FFFFFFF:
-        raise ValueError("window and sinks must be below 2^31")
+    if not (-0x80000000 <= window <= 0x7FFFFFFF and -0x80000000 <= sinks <= 0x7FFFFFFF
+            and -0x80000000 <= s_q <= 0x7FFFFFFF and -0x80000000 <= H <= 0x7FFFFFFF):
+        raise ValueError("window, sinks, s_q and H must lie in [-2^31, 2^31)")
 
 
 def rope_q(q, cache_seqlens, rope: Rope, q_lens=None, q_heads=None, q_pe=None, status=None, stream=None):
@@ -671,7 +672,7 @@ def get_metadata_window(cache_seqlens, q_lens, s_q: int, H: int, window: int, si
     """mla_get_metadata_window: the schedule for decode_window / decode_fp8_window (shared by
     every layer of a step); q_lens may be None."""
     i32 = (_torch or _torch_module()).int32
-    _window_range(window, sinks)
+    _window_range(window, sinks, s_q, H)
     (B,) = cache_seqlens.shape
     index = _device_index(cache_seqlens)
     handle = _launch_stream(index, stream)

@@ -220,3 +220,22 @@ def test_window_sizes_beyond_an_int_are_refused(window, sinks):
                         (mla.decode_fp8_window, torch.zeros(1, 64, 656, dtype=torch.uint8))):
         with pytest.raises(ValueError, match="2\\^31"):
             call(q, q[..., :64].contiguous(), cache, torch.zeros(2, 1, dtype=torch.int32), n, None, 0.1, window, sinks, n)
+
+
+@pytest.mark.parametrize("s_q,H,window,sinks", [
+    (1, 16, -(2**32) + 100, 4), (1, 16, 100, -(2**32) + 4), (1, 16, -(2**31) - 1, 0), (1, 16, 100, -(2**40)),
+    (2**32 + 1, 16, 100, 4), (1, 2**32 + 16, 100, 4), (-(2**32) + 1, 16, 100, 4), (1, -(2**32) + 16, 100, 4),
+])
+def test_window_sizes_below_an_int_and_shapes_beyond_one_are_refused(s_q, H, window, sinks):
+    """A C int would cut them too: -2^32 + 100 keys to 100, 2^32 + 16 heads to 16."""
+    torch = pytest.importorskip("torch")
+    n = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="2\\^31"):
+        mla.get_metadata_window(n, None, s_q, H, window, sinks)
+    if (s_q, H) == (1, 16):
+        q = torch.zeros(2, 1, 16, 512, dtype=torch.bfloat16)
+        for call, cache in ((mla.decode_window, torch.zeros(1, 64, 576, dtype=torch.bfloat16)),
+                            (mla.decode_fp8_window, torch.zeros(1, 64, 656, dtype=torch.uint8))):
+            with pytest.raises(ValueError, match="2\\^31"):
+                call(q, q[..., :64].contiguous(), cache, torch.zeros(2, 1, dtype=torch.int32), n, None, 0.1, window,
+                     sinks, n)
