@@ -8,11 +8,13 @@
 // 656 written a row.
 //
 // Measured: 65536 rows with norm and rotation in 29.7 us, 5.1 TB/s, 78 % of a plain copy
-// (25.4 us without the two: instructions are issued in two cycles of three, so norm and
-// rotation still cost 4 us); 20 k FP8 rows in 13 us, whose 16 codes a lane are products
+// (25.4 us without the two); 20 k FP8 rows in 12.6 us, whose 16 codes a lane are products
 // instead of divisions where that decides them (17.2 us with divisions); a decode step's 256
 // rows in 2.4 us, a launch.  Two rows a warp (30.5 us) and persistent warps that load a row
-// ahead (36 us) lose to more warps: 48 registers keep 40 of them on an SM.
+// ahead (36 us) lose to more warps: 48 registers keep 40 of them on an SM.  What bounds both
+// is latency: 33 warps run at a time, an instruction waits 14 to 15 cycles, 4 to 5 of them for
+// loads and 4 for the butterflies, and the issue slots are busy in 54 % (bf16) and 58 % (FP8) of
+// the cycles, DRAM at 42 % and 16 % of its rate.
 //
 // One warp per row.  Lane l holds c[8l..8l+7] and c[256+8l..256+8l+7] (two 16-byte loads,
 // and 8- or 16-byte stores, contiguous over the warp) and pair l of k; the sum of squares
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32) append_kernel(const __gri
   float c0[8], c1[8];
   unpack8(v0, c0);
   unpack8(v1, c1);
-  if (p.weight) {  // in packed pairs: the kernel issues instructions two thirds of the time
+  if (p.weight) {  // in packed pairs: half the issue slots of the scalar form
     float w0[8], w1[8];
     unpack8(reinterpret_cast<const uint4*>(p.weight)[lane], w0);
     unpack8(reinterpret_cast<const uint4*>(p.weight)[lane + 32], w1);

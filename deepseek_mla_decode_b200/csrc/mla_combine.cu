@@ -40,7 +40,8 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
 // in flight per lane (32 registers of loads for one warp per row and two splits, 64 for
 // four warps per row and sixteen splits); kBySeq: block x is a sequence (else a
 // partition); kWin: of a windowed schedule.  The one-warp kernels are held to 64 registers
-// (four blocks on an SM: with 76 the merge of 64 sequences took 1.1 us longer)
+// (four blocks on an SM: with 76 the merge of 64 sequences took 1.1 us longer), at 12 bytes of
+// spills in the windowed one by sequences
 template <int kColParts, int kGroup, bool kBySeq, bool kWin>
 __global__ void __launch_bounds__(kWarps * 32, kColParts == 1 ? 4 : 2) combine_kernel(
     const int32_t* __restrict__ meta, const int32_t* __restrict__ seqlens, const int32_t* __restrict__ q_lens,

@@ -5,13 +5,16 @@
 //     (a, b) -> (a cos t - b sin t, a sin t + b cos t) * amplitude,   t = p * freq[i]
 // A position of 10^5 with a frequency near 1 is tens of thousands of turns, of which
 // fp32 would keep two digits.  Only the fraction of a turn counts, so a frequency is kept as
-// its fraction of a turn a position in units of 2^-64 (rounded on the host from extended
-// precision), and p times it modulo 2^64 is the angle's fraction, exact but for p 2^-65: one
-// integer product instead of fp64 arithmetic and its conversions.  The upper 32 bits as a
+// its fraction of a turn a position, cut on the host from extended precision to 2^-63 of a turn
+// (towards zero; in units of 2^-64, whose last bit is 0), and p times it modulo 2^64 is the
+// angle's fraction, off by less than p 2^-63 of a turn for frequencies up to a turn a position
+// (2^-32 of a turn at the largest p; a frequency of k turns keeps log2 k bits less): one integer
+// product instead of fp64 arithmetic and its conversions.  The upper 32 bits as a
 // signed number are the angle in [-1/2, 1/2) turns, which goes to fp32 (angle error
 // pi 2^-24) and, being within [-pi, pi], to the fast sine and cosine (absolute error 2^-21.2
-// there by CUDA's documentation).  Together under 2^-20.5 of a value, 2^12 times below a bf16
-// half step; the accurate functions took 45 of the append's 290 instructions a row.
+// there by CUDA's documentation).  Together under 2^-20.5 of the pair's length, 2^12 times below
+// a bf16 half step of it; a component that the rotation takes close to 0 keeps that absolute
+// error.  The accurate functions took 45 of the append's 290 instructions a row.
 #pragma once
 #include <cuda_runtime.h>
 #include <cstdint>

@@ -29,14 +29,18 @@
 // and dims 256h + 128r + (0..127) as its half of the PV operand.  One box of the cache, 64
 // rows x 128 code bytes, serves both: K-major for QK, MN-major for PV.
 //
-// Measured (192 sequences, 128 heads, window 4096, attention and combine): 261-270 us,
+// Measured (192 sequences, 128 heads, window 4096, attention and combine): 262-272 us,
 // 49 % of the tensor floor, against 432 us for the kernel that converts codes to
-// bf16.  No unit is busy half the time (tensor pipe 45 %, issue 39 %, DRAM 28 %); a tile of
+// bf16; with scores six times as wide 263-274 us.  128 sequences with up to four draft tokens,
+// window 512: 134-146 us against a floor of 33, and 256 sequences, window 1024: 145 us against
+// 44, both more than the bf16 cache's 100 and 117 us: a piece of five tiles or less is mostly
+// its switch.  No unit is busy half the time (tensor pipe 45 %, issue 35 %, DRAM 27 %); a tile of
 // 9.7 k cycles is the softmax's two passes (5 k), its hand-offs (3 k) and, spread over 13
 // tiles, the switch of pieces (0.9 k: the new query's terms and the old output).  The
 // instruction stream is part of it: with both passes unrolled over 64 keys and the terms made
 // by unrolled code the kernel took 346 us, for the warps waited for instructions; so the
-// passes run over groups of 16 and 32 keys and read the scores from tensor memory twice.
+// passes run over groups of 16 and 32 keys and read the scores from tensor memory twice.  128
+// registers a thread at compile time leave 24 bytes of spills.
 //
 // Warps: 0, 2, 3 producers, 1 MMA issue (leader) and TMEM, 4..11 softmax and epilogue,
 // 12..15 preparation (the query rows' terms once a piece; the rotary keys' terms and the

@@ -206,12 +206,15 @@ mla_status_t mla_decode_fp8_tokens(const void* q_nope, const void* q_pe, const v
  * table entries may be stale), and hidden rows of the blocks at a window's edges never
  * reach a result, whatever they hold.
  *
- *   window  >= 64 (smaller: MLA_ERR_UNSUPPORTED);  sinks >= 0
+ *   window  >= 64 (smaller: MLA_ERR_UNSUPPORTED);  sinks >= 0;  s_q <= 4 as in every decode
+ *   (mla_sage_prefill has no window)
  * mla_get_metadata_window: the schedule, for the same cache_seqlens, q_lens (NULL: s_q
  *   each), window and sinks; mla_metadata_size(B * s_q, 1, H) bytes.
  * mla_decode_window, mla_decode_fp8_window: over the bf16 and the packed FP8 cache; the
  *   workspace holds mla_workspace_size(B * s_q, 1, H) bytes.  The split partials are merged
- *   by the LSE combine as in mla_decode.  Device errors as in mla_decode_tokens (metadata
+ *   by the LSE combine as in mla_decode.  Over the FP8 cache a weight times its row's scale is
+ *   held to 2^-8 of itself or 2^-16 of the largest within its tile of 256 visible keys, a query
+ *   value to bf16's bits or 2^-21 of its row's largest.  Device errors as in mla_decode_tokens (metadata
  *   of another schedule, window or sinks: MLA_DEVICE_ERR_METADATA, and where that can be
  *   told from the header alone nothing is written).
  */
@@ -459,7 +462,8 @@ mla_status_t mla_rope_init(mla_rope_t* rope, double base, int half_layout, int s
  *   Tokens without a place get zeros, those of a sequence with an invalid length or count
  *   NaN.  1 <= H <= 65535; the outputs must not overlap q.
  * mla_rope_inplace: rotates the 64 of each head of q where they lie (for the quantised
- *   prefill's q and k); the 128 are not touched.
+ *   prefill's q and k); the 128 are not touched.  The 64 of tokens without a place become
+ *   zeros, those of a sequence with an invalid length or count NaN.
  * All pointers are device pointers, 16-byte aligned; asynchronous on `stream`.
  */
 mla_status_t mla_rope_q(const void* q, int64_t row_stride, const int32_t* cache_seqlens, const int32_t* q_lens, int B,
