@@ -15,9 +15,9 @@
 //   PV:  P = 2^(x - m) * s = P_hi + P_lo.  Every key counts: where one key takes most of the
 //        weight (the first keys, which are kept visible for that), thousands share the rest, and
 //        a grid fixed by the largest loses them.  So m follows the largest x + log2 s of each
-//        tile, up and down, lazily: a tile's largest P stays in [2^2, 2^8.5), O is rescaled
-//        when it would leave that, and a weight is off by at most 2^-8 of itself or 2^-16 of
-//        its tile's largest (a tile's 256 keys together lose less than 2^-8 of that one).  The
+//        tile, up and down, lazily: a tile's largest P stays in [2^6, 2^8.5), O is rescaled
+//        when it would leave that, and a weight is off by at most 2^-8 of itself or 2^-20 of
+//        its tile's largest (a tile's 256 keys together lose less than 2^-12 of that one).  The
 //        normaliser l = sum 2^(x - m) is fp32, in the unit of the row's largest.
 // Two 8-bit MMAs take the time of one bf16 MMA, so this costs no tensor time over the bf16
 // cache, moves half its bytes through the ring, and converts nothing but the 64 rotary
@@ -31,7 +31,7 @@
 //
 // Measured (192 sequences, 128 heads, window 4096, attention and combine): 262-272 us,
 // 49 % of the tensor floor, against 432 us for the kernel that converts codes to
-// bf16; with scores six times as wide 263-274 us.  128 sequences with up to four draft tokens,
+// bf16; with scores six times as wide 265-281 us.  128 sequences with up to four draft tokens,
 // window 512: 134-146 us against a floor of 33, and 256 sequences, window 1024: 145 us against
 // 44, both more than the bf16 cache's 100 and 117 us: a piece of five tiles or less is mostly
 // its switch.  No unit is busy half the time (tensor pipe 45 %, issue 35 %, DRAM 27 %); a tile of
@@ -87,11 +87,12 @@ constexpr int kRegsIssue = 88, kRegsPrep = 88, kRegsSoftmax = 168;
 static_assert(128 * (kRegsIssue + kRegsPrep) + 256 * kRegsSoftmax == kThreads * 128, "register split");
 constexpr uint32_t kTmemO = 0, kTmemS0 = 256, kTmemCols = 512;
 // The largest P of a tile is 2^kHeadroom where a unit is taken and stays in
-// [2^(kHeadroom - kFall), 2^(kHeadroom + kRise)) = [2^2, 2^8.5) while it is kept: below e4m3's
-// 448, and high enough for e5m2's smallest steps.  Units taken at 2^5 to 2^7.5 within these
-// bounds cost the same (262.0 to 262.8 us, 192 sequences); higher ones are finer, but O is
-// rescaled sooner where scores grow along the window.
-constexpr float kHeadroom = 6.0f, kRise = 2.5f, kFall = 4.0f;
+// [2^(kHeadroom - kFall), 2^(kHeadroom + kRise)) = [2^6, 2^8.5) while it is kept: below e4m3's
+// 448, and as far above e5m2's smallest steps as that allows.  O is rescaled the more often, which
+// costs little: 269.4 us (192 sequences) against 268.1 with the unit at 2^6 in [2^2, 2^8.5), and
+// 269.1 against 267.9 where every other tile's scales are 2^-12 of the others', so that each
+// tile takes a new unit.
+constexpr float kHeadroom = 8.0f, kRise = 0.5f, kFall = 2.0f;
 // The unit falls at most this far below the row's largest: what a tile below that adds is not
 // worth its exponent (2^-40 a key), and O stays far from fp32's range.
 constexpr float kUnitFloor = 40.0f;

@@ -213,7 +213,7 @@ mla_status_t mla_decode_fp8_tokens(const void* q_nope, const void* q_pe, const v
  * mla_decode_window, mla_decode_fp8_window: over the bf16 and the packed FP8 cache; the
  *   workspace holds mla_workspace_size(B * s_q, 1, H) bytes.  The split partials are merged
  *   by the LSE combine as in mla_decode.  Over the FP8 cache a weight times its row's scale is
- *   held to 2^-8 of itself or 2^-16 of the largest within its tile of 256 visible keys, a query
+ *   held to 2^-8 of itself or 2^-20 of the largest within its tile of 256 visible keys, a query
  *   value to bf16's bits or 2^-21 of its row's largest.  Device errors as in mla_decode_tokens (metadata
  *   of another schedule, window or sinks: MLA_DEVICE_ERR_METADATA, and where that can be
  *   told from the header alone nothing is written).
@@ -416,8 +416,10 @@ mla_status_t mla_sage_prefill(const void* q, const void* k, const void* v, int S
  *     (a, b) -> amplitude * (a cos t - b sin t, a sin t + b cos t),   t = p * freq[i]
  * with (a, b) = (x[2i], x[2i + 1]) or, with half_layout, (x[i], x[i + 32]); the result is in
  * the same layout.  Angles are formed and reduced in 64 bits, the rotation is fp32, the
- * result is rounded once.  A mla_rope_t is host memory, read before the call returns; fill
- * it with mla_rope_init or by hand (|freq| <= 1e6 radians a position, finite amplitude).
+ * result is rounded once (error before that: under 2^-20.5 of the pair's length, for
+ * frequencies up to a turn a position).  A mla_rope_t is host memory, read before the call
+ * returns; fill it with mla_rope_init or by hand (|freq| <= 1e6 radians a position, finite
+ * amplitude).
  *
  * mla_rope_init: freq[i] = base^(-i/32), then
  *   MLA_ROPE_PLAIN   as it is (factor and the rest are not looked at)

@@ -5,8 +5,8 @@ they carry may be all there is to see.
 What is allowed.  Over the FP8 cache the kernel holds the weight of a key, times the key's scale (P = w s), in two
 terms whose unit follows the largest P of its tile of 256 keys.  A weight is off by at most half
 a step of bf16's eight bits, 2^-8 P (the four bits of e4m3 and the three and a sign of e5m2), or
-2^-16 of the tile's largest where that is more (e5m2's half step 2^-14 below 2^-10, the largest
-kept at 2^2 or above), and never by more than P itself.  Added up over the keys this bounds an
+2^-20 of the tile's largest where that is more (e5m2's half step 2^-14 below 2^-10, the largest
+kept at 2^6 or above), and never by more than P itself.  Added up over the keys this bounds an
 output, with the bf16 rounding of the result (2^-8) and 2^-14 of sum |w c| for what fp32 scores,
 exponentials and sums of a few dozen bits' range leave.  Over the bf16 cache a weight is off by
 2^-8 of itself, and so is their sum, which is of the rounded ones.  Neither bound grows with the
@@ -114,7 +114,7 @@ class OneKeyAhead:
             for d in range(1, TILE):
                 top[..., d:] = np.maximum(top[..., d:], P[..., :-d])
                 top[..., :-d] = np.maximum(top[..., :-d], P[..., d:])
-        err = np.minimum(P, np.maximum(2.0 ** -8 * P, 2.0 ** -16 * top)) / self.scales[t]
+        err = np.minimum(P, np.maximum(2.0 ** -8 * P, 2.0 ** -20 * top)) / self.scales[t]
         return ref[0], ref[1], (err @ c)[:, None] + rounding
 
     def check(self, B, window, sinks, bars=True):
